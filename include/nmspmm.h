@@ -42,7 +42,13 @@ typedef enum {
     NM_ERR_TIMEOUT = 5      /* a kernel gave up a bounded wait (see nm_device_status) */
 } nm_status;
 
-typedef enum { NM_INT8 = 0, NM_FP16 = 1, NM_BF16 = 2 } nm_dtype;
+typedef enum {
+    NM_INT8 = 0,
+    NM_FP16 = 1,
+    NM_BF16 = 2,
+    NM_FP32 = 3,            /* nm_compress_mx, nm_mx_quantize and nm_mx_dequantize only */
+    NM_MXFP4 = 4            /* what nm_query reports for a handle of nm_compress_mx    */
+} nm_dtype;
 
 /* Opaque handle holding one compressed weight; owns all device memory it allocates. */
 typedef struct nm_handle nm_handle;
@@ -179,7 +185,12 @@ typedef enum {
   NM_OUT_INT8 = 5
 } nm_out_type;
 
-typedef enum { NM_ACT_NONE = 0, NM_ACT_GELU = 1 } nm_act;
+typedef enum {
+  NM_ACT_NONE = 0,
+  NM_ACT_GELU = 1,
+  NM_ACT_SILU = 2,     /* gated products only: v / (1 + exp(-v)) */
+  NM_ACT_RELU = 3      /* gated products only: max(v, 0)         */
+} nm_act;
 
 typedef struct nm_epilogue {
   nm_out_type out;     /* element type of Y */
@@ -264,6 +275,84 @@ nm_status nm_spmm_gather(const nm_handle* h, const void* Xt_dev, int64_t ldx, in
  */
 nm_status nm_spmm_gather_ex(const nm_handle* h, const void* Xt_dev, int64_t ldx, int64_t T, void* Y_dev,
                             const nm_epilogue* ep, void* stream);
+
+/*
+ * Microscaled 4-bit floating point (the MXFP4 format of the OCP Microscaling
+ * Formats specification, version 1.0).  (No counterpart in the paper: it is a
+ * further storage format for the same linears.)  Along k, every block of 32
+ * values shares one scale 2^e, kept as the byte e + 127 (E8M0); a value is a
+ * 4-bit code (E2M1): a sign and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (codes 0 to 7
+ * in that order, the sign in bit 3).  Quantisation:
+ *   e    = floor(log2(max |x| of the block)) - 2, at least -127
+ *   code = x / 2^e rounded to the nearest of those, a tie to the even code;
+ *          above 6 it becomes 6
+ * A block of zeros has scale byte 0.  A block that holds an infinity or a NaN
+ * has scale byte 255 (which makes every value of the block NaN) and codes 0.
+ * All of it is exact arithmetic, so the result does not depend on the GPU.
+ *
+ * Layout of a quantised matrix [rows][k]:
+ *   codes   [rows][k / 2] bytes, two per byte, the lower k in the low nibble;
+ *   scales  tiles of 128 rows x 256 k (1024 bytes), row tiles outermost: the
+ *           byte of row r and block b (k in [32b, 32b + 32)) is at
+ *             ((r / 128) * ceil(k / 256) + b / 8) * 1024 + ((b % 8) / 4) * 512
+ *             + (r % 32) * 16 + ((r % 128) / 32) * 4 + b % 4,
+ *           which is how the tensor core reads them.  Bytes of rows and blocks
+ *           beyond the matrix are 0.  nm_mx_scale_bytes gives the total.
+ */
+nm_status nm_mx_scale_bytes(int64_t rows, int64_t k, size_t* bytes);
+
+/*
+ * nm_mx_quantize -- X [T][k] (row stride ldx elements; NM_FP32, NM_FP16 or
+ * NM_BF16) to codes Q_dev [T][k / 2] and scales S_dev (nm_mx_scale_bytes(T, k)
+ * bytes, all written).  k > 0 and a multiple of 32, ldx >= k, ldx * sizeof a
+ * multiple of 16 bytes, all pointers 16-byte aligned, T >= 0 (0 is a no-op),
+ * else NM_ERR_INVALID.  Q and S must not overlap X.
+ */
+nm_status nm_mx_quantize(const void* X_dev, int64_t T, int64_t k, int64_t ldx, nm_dtype dt, void* Q_dev,
+                         void* S_dev, void* stream);
+
+/*
+ * nm_mx_dequantize -- the values that codes and scales stand for, into X_dev
+ * [T][k] of type dt (NM_FP32 and NM_BF16 hold every one exactly; NM_FP16 rounds
+ * to nearest even).  Arguments as nm_mx_quantize with ldx = k.
+ */
+nm_status nm_mx_dequantize(const void* Q_dev, const void* S_dev, int64_t T, int64_t k, nm_dtype dt, void* X_dev,
+                           void* stream);
+
+/*
+ * nm_compress_mx -- prune W [n_out][k] (NM_FP32, NM_FP16 or NM_BF16) to N:M by
+ * nm_compress's rule (N == M keeps everything), quantise what is kept as above
+ * and lay it out for nm_spmm_mx.  (N, M) as nm_compress; k a multiple of 32,
+ * at most 2^24 (n_out too); W 16-byte aligned.
+ * gated != 0: W is [2 n_ff][k], the n_ff gate rows first (n_out = 2 n_ff, even),
+ * and the handle's product is nm_spmm_mx_gated.
+ * nm_recompress (W of the same type), nm_decompress (the pruned, quantised
+ * values as BF16, which holds them exactly), nm_query (reports NM_MXFP4),
+ * nm_device_status and nm_destroy accept the handle; the other calls reject it.
+ */
+nm_status nm_compress_mx(const void* W_dev, int64_t n_out, int64_t k, nm_dtype dt, int N, int M, int gated,
+                         void* stream, nm_handle** out);
+
+/*
+ * nm_spmm_mx -- Y = X . Wm^T with X given quantised (codes Q_dev [T][k / 2] and
+ * scales S_dev of nm_mx_quantize) and the handle's quantised weight: products
+ * of 4-bit values times their blocks' scales, summed in fp32, then the fused
+ * output stage of nm_spmm_ex (scale, bias, NM_ACT_GELU; fp32, fp16 or bf16).
+ * NM_OUT_DEFAULT is the type of the handle's source weight; ep == NULL is that
+ * with nothing else.  Y_dev [T][n_out], 16-byte aligned, overlapping neither Q
+ * nor S; T >= 0 (0 is a no-op).  Allocates nothing, never synchronises, keeps
+ * nothing between calls: calls on one handle may overlap.
+ */
+nm_status nm_spmm_mx(const nm_handle* h, const void* Q_dev, const void* S_dev, int64_t T, void* Y_dev,
+                     const nm_epilogue* ep, void* stream);
+
+/*
+ * nm_spmm_mx_gated -- the gated block of nm_spmm_gated for a gated handle of
+ * nm_compress_mx: Y [T][n_ff] = act(g) * u.  ep as in nm_spmm_gated (scale and
+ * bias are [2 n_ff]); fp32, fp16 or bf16 output.  Otherwise as nm_spmm_mx.
+ */
+nm_status nm_spmm_mx_gated(const nm_handle* h, const void* Q_dev, const void* S_dev, int64_t T, void* Y_dev,
+                           const nm_epilogue* ep, void* stream);
 
 /*
  * nm_decompress -- write the masked dense weight Wm [n_out][k] (dtype of the

@@ -19,15 +19,17 @@ LIB_PATH = os.path.join(_HERE, "libnmspmm.so")
 NM_OK, NM_ERR_INVALID, NM_ERR_UNSUPPORTED, NM_ERR_CUDA, NM_ERR_OOM, NM_ERR_TIMEOUT = range(6)
 STATUS_NAMES = {0: "NM_OK", 1: "NM_ERR_INVALID", 2: "NM_ERR_UNSUPPORTED", 3: "NM_ERR_CUDA",
                 4: "NM_ERR_OOM", 5: "NM_ERR_TIMEOUT"}
-NM_INT8, NM_FP16, NM_BF16 = 0, 1, 2
+NM_INT8, NM_FP16, NM_BF16, NM_FP32, NM_MXFP4 = 0, 1, 2, 3, 4
 _TORCH_DT = {torch.int8: NM_INT8, torch.float16: NM_FP16, torch.bfloat16: NM_BF16}
+_MX_DT = {torch.float16: NM_FP16, torch.bfloat16: NM_BF16, torch.float32: NM_FP32}
 _ELEM = {NM_INT8: torch.int8, NM_FP16: torch.float16, NM_BF16: torch.bfloat16}
 
 # Every symbol include/nmspmm.h declares.
 EXPORTS = ("nm_compress", "nm_compress_tile", "nm_recompress", "nm_spmm", "nm_spmm_ex", "nm_spmm_gather",
            "nm_spmm_gather_ex", "nm_spmm_noalloc", "nm_decompress", "nm_export", "nm_export_sizes", "nm_query",
            "nm_plan_query", "nm_plan_for_shape", "nm_device_status", "nm_destroy", "nm_last_error", "nm_version",
-           "nm_test_spmm_skip_stage")
+           "nm_test_spmm_skip_stage", "nm_mx_scale_bytes", "nm_mx_quantize", "nm_mx_dequantize", "nm_compress_mx",
+           "nm_spmm_mx", "nm_spmm_mx_gated")
 
 
 class NMPlanInfo(ctypes.Structure):
@@ -71,6 +73,12 @@ def lib() -> ctypes.CDLL:
         L.nm_plan_query.argtypes = [vp, i64, i32, ctypes.POINTER(NMPlanInfo)]
         L.nm_plan_for_shape.argtypes = [i32, i64, i64, i32, i32, i64, i32, ctypes.POINTER(i32), ctypes.POINTER(i32),
                                         ctypes.POINTER(NMPlanInfo)]
+        L.nm_mx_scale_bytes.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_size_t)]
+        L.nm_mx_quantize.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp]
+        L.nm_mx_dequantize.argtypes = [vp, vp, i64, i64, i32, vp, vp]
+        L.nm_compress_mx.argtypes = [vp, i64, i64, i32, i32, i32, i32, vp, ctypes.POINTER(vp)]
+        L.nm_spmm_mx.argtypes = [vp, vp, vp, i64, vp, ctypes.POINTER(NMEpilogue), vp]
+        L.nm_spmm_mx_gated.argtypes = [vp, vp, vp, i64, vp, ctypes.POINTER(NMEpilogue), vp]
         L.nm_device_status.argtypes = [vp]
         L.nm_destroy.argtypes = [vp]
         L.nm_destroy.restype = None
@@ -79,7 +87,8 @@ def lib() -> ctypes.CDLL:
         for name in ("nm_compress", "nm_compress_tile", "nm_recompress", "nm_spmm", "nm_spmm_gather",
                      "nm_spmm_gather_ex", "nm_spmm_noalloc",
                      "nm_test_spmm_skip_stage", "nm_decompress", "nm_export", "nm_export_sizes", "nm_query",
-                     "nm_plan_query", "nm_plan_for_shape", "nm_device_status"):
+                     "nm_plan_query", "nm_plan_for_shape", "nm_device_status", "nm_mx_scale_bytes", "nm_mx_quantize",
+                     "nm_mx_dequantize", "nm_compress_mx", "nm_spmm_mx", "nm_spmm_mx_gated"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -102,13 +111,34 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An output that belongs to the stream the call runs on (torch's allocator
+    then never hands its memory to work that is not ordered behind it)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _check_tensor(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> None:
+    """A contiguous tensor of this type and shape on the current CUDA device."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+
+
 class NMHandle:
     """One compressed weight (owns the library handle and its device memory)."""
 
-    def __init__(self, raw: int, n_out: int, k: int, N: int, M: int, dt: int, tile: bool = False):
+    def __init__(self, raw: int, n_out: int, k: int, N: int, M: int, dt: int, tile: bool = False,
+                 gated: bool = False, src: torch.dtype | None = None):
         self._raw = ctypes.c_void_p(raw)
         self.n_out, self.k, self.N, self.M, self.dt = n_out, k, N, M, dt
         self.tile = tile  # one pattern per 128-channel tile (nm_compress_tile)
+        self.gated = gated  # rows [0, n_out / 2) gate, the rest up
+        self.src = src  # microscaled handles: the element type of the source weight
 
     @property
     def raw(self) -> ctypes.c_void_p:
@@ -118,7 +148,8 @@ class NMHandle:
 
     @property
     def dtype(self) -> torch.dtype:
-        return _ELEM[self.dt]
+        """Element type of the weight it is made from."""
+        return self.src if self.src is not None else _ELEM[self.dt]
 
     def destroy(self) -> None:
         if self._raw and _lib is not None:
@@ -170,7 +201,7 @@ def nm_recompress(h: NMHandle, W: torch.Tensor, stream=None) -> NMHandle:
 def out_dtype(h: NMHandle, scaled: bool) -> torch.dtype:
     if h.dt == NM_INT8:
         return torch.float32 if scaled else torch.int32
-    return _ELEM[h.dt]
+    return h.dtype
 
 
 def nm_spmm(h: NMHandle, X: torch.Tensor, Y: torch.Tensor | None = None, scale: torch.Tensor | None = None,
@@ -217,7 +248,7 @@ class NMEpilogue(ctypes.Structure):
 
 
 OUT_TYPES = {"default": 0, "int32": 1, "float32": 2, "float16": 3, "bfloat16": 4, "int8": 5}
-ACTS = {"none": 0, "gelu": 1}
+ACTS = {"none": 0, "gelu": 1, "silu": 2, "relu": 3}  # silu and relu: gated products only
 _OUT_TORCH = {"int32": torch.int32, "float32": torch.float32, "float16": torch.float16,
               "bfloat16": torch.bfloat16, "int8": torch.int8}
 
@@ -280,6 +311,116 @@ def nm_spmm_gather_ex(h: NMHandle, Xt: torch.Tensor, T: int | None = None, Y: to
     return Y
 
 
+def _epilogue(h: NMHandle, scale, bias, act: str, out: str, out_scale: float) -> NMEpilogue:
+    """``nm_epilogue`` of a call on ``h`` after checking what the C side cannot see."""
+    if out not in OUT_TYPES or act not in ACTS:
+        raise ValueError(f"out must be one of {tuple(OUT_TYPES)}, act one of {tuple(ACTS)}")
+    if scale is not None:
+        _check_tensor("scale", scale, torch.float32, (h.n_out,))
+    if bias is not None:
+        _check_tensor("bias", bias, torch.float32, (h.n_out,))
+    return NMEpilogue(OUT_TYPES[out], ACTS[act], _ptr(scale), _ptr(bias), float(out_scale))
+
+
+def nm_mx_scale_bytes(rows: int, k: int) -> int:
+    """Bytes of the scales of a microscaled [rows, k] matrix (layout in include/nmspmm.h)."""
+    n = ctypes.c_size_t()
+    _check(lib().nm_mx_scale_bytes(int(rows), int(k), ctypes.byref(n)))
+    return n.value
+
+
+def nm_mx_quantize(X: torch.Tensor, Q: torch.Tensor | None = None, S: torch.Tensor | None = None,
+                   stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """X [T, k] (fp32 / fp16 / bf16, rows contiguous, any row stride that is a
+    multiple of 16 bytes) to microscaled 4-bit codes Q [T, k / 2] and scales S (uint8)."""
+    if X.dim() != 2 or X.dtype not in _MX_DT or (X.shape[1] > 1 and X.stride(1) != 1):
+        raise ValueError("X must be a [T, k] float32/float16/bfloat16 tensor with contiguous rows")
+    if X.get_device() != torch.cuda.current_device():
+        raise ValueError("X must be on the current CUDA device")
+    T, k = X.shape
+    n = (T + 127) // 128 * ((k + 255) // 256) * 1024
+    if Q is None:
+        Q = _empty((T, k // 2), torch.uint8, X.device, stream)
+    else:
+        _check_tensor("Q", Q, torch.uint8, (T, k // 2))
+    if S is None:
+        S = _empty((n,), torch.uint8, X.device, stream)
+    else:
+        _check_tensor("S", S, torch.uint8, (n,))
+    ldx = X.stride(0) if T > 1 else k
+    _check(lib().nm_mx_quantize(X.data_ptr(), T, k, ldx, _MX_DT[X.dtype], Q.data_ptr(), S.data_ptr(),
+                                _stream(stream)))
+    return Q, S
+
+
+def _check_mx(Q: torch.Tensor, S: torch.Tensor) -> tuple[int, int]:
+    if Q.dim() != 2:
+        raise ValueError("Q must be [T, k / 2]")
+    T, k = Q.shape[0], 2 * Q.shape[1]
+    _check_tensor("Q", Q, torch.uint8, (T, k // 2))
+    _check_tensor("S", S, torch.uint8, ((T + 127) // 128 * ((k + 255) // 256) * 1024,))
+    return T, k
+
+
+def nm_mx_dequantize(Q: torch.Tensor, S: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                     X: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values that codes and scales of ``nm_mx_quantize`` stand for."""
+    if dtype not in _MX_DT:
+        raise ValueError("dtype must be float32, float16 or bfloat16")
+    T, k = _check_mx(Q, S)
+    if X is None:
+        X = _empty((T, k), dtype, Q.device, stream)
+    else:
+        _check_tensor("X", X, dtype, (T, k))
+    _check(lib().nm_mx_dequantize(Q.data_ptr(), S.data_ptr(), T, k, _MX_DT[dtype], X.data_ptr(), _stream(stream)))
+    return X
+
+
+def nm_compress_mx(W: torch.Tensor, N: int = 4, M: int = 4, gated: bool = False, stream=None) -> NMHandle:
+    """Prune W [n_out, k] (fp32 / fp16 / bf16) to N:M, quantise it to microscaled
+    4-bit values and pack it for ``nm_spmm_mx`` (``gated``: rows [0, n_out / 2)
+    gate, the rest up, for ``nm_spmm_mx_gated``)."""
+    if W.dim() != 2 or W.dtype not in _MX_DT:
+        raise ValueError("W must be a [n_out, k] float32/float16/bfloat16 tensor")
+    _check_tensor("W", W, W.dtype, tuple(W.shape))
+    n_out, k = W.shape
+    out = ctypes.c_void_p()
+    _check(lib().nm_compress_mx(W.data_ptr(), n_out, k, _MX_DT[W.dtype], N, M, int(bool(gated)), _stream(stream),
+                                ctypes.byref(out)))
+    return NMHandle(out.value, n_out, k, N, M, NM_MXFP4, gated=bool(gated), src=W.dtype)
+
+
+def _mx_product(name: str, h: NMHandle, Q, S, Y, scale, bias, act: str, out: str, stream) -> torch.Tensor:
+    T, k = _check_mx(Q, S)
+    if k != h.k:
+        raise ValueError(f"Q holds k = {k}, the handle {h.k}")
+    ep = _epilogue(h, scale, bias, act, out, 1.0)
+    want = h.dtype if out == "default" else _OUT_TORCH[out]
+    n = h.n_out // 2 if name == "nm_spmm_mx_gated" else h.n_out
+    if Y is None:
+        Y = _empty((T, n), want, Q.device, stream)
+    else:
+        _check_tensor("Y", Y, want, (T, n))
+    _check(getattr(lib(), name)(h.raw, Q.data_ptr(), S.data_ptr(), T, Y.data_ptr(), ctypes.byref(ep),
+                                _stream(stream)))
+    return Y
+
+
+def nm_spmm_mx(h: NMHandle, Q: torch.Tensor, S: torch.Tensor, Y: torch.Tensor | None = None,
+               scale: torch.Tensor | None = None, bias: torch.Tensor | None = None, act: str = "none",
+               out: str = "default", stream=None) -> torch.Tensor:
+    """Y = out(act(X @ Wm^T * scale + bias)) for a handle of ``nm_compress_mx`` and
+    X given as the codes Q and scales S of ``nm_mx_quantize``."""
+    return _mx_product("nm_spmm_mx", h, Q, S, Y, scale, bias, act, out, stream)
+
+
+def nm_spmm_mx_gated(h: NMHandle, Q: torch.Tensor, S: torch.Tensor, Y: torch.Tensor | None = None,
+                     scale: torch.Tensor | None = None, bias: torch.Tensor | None = None, act: str = "silu",
+                     out: str = "default", stream=None) -> torch.Tensor:
+    """Y [T, n_out / 2] = act(gate) * up for a gated handle of ``nm_compress_mx``."""
+    return _mx_product("nm_spmm_mx_gated", h, Q, S, Y, scale, bias, act, out, stream)
+
+
 def nm_spmm_noalloc(h: NMHandle, X: torch.Tensor, Y: torch.Tensor, scale: torch.Tensor | None = None,
                     stream=None) -> torch.Tensor:
     """nm_spmm for callers that cannot allocate: split-K scratch lives in a fixed
@@ -297,7 +438,8 @@ def nm_test_spmm_skip_stage(h: NMHandle, X: torch.Tensor, Y: torch.Tensor, scale
 
 def nm_decompress(h: NMHandle, stream=None) -> torch.Tensor:
     """Masked dense W decoded from the packed operand image the SpMM reads."""
-    out = torch.empty((h.n_out, h.k), dtype=h.dtype, device="cuda")
+    dtype = torch.bfloat16 if h.dt == NM_MXFP4 else h.dtype
+    out = torch.empty((h.n_out, h.k), dtype=dtype, device="cuda")
     _check(lib().nm_decompress(h.raw, _ptr(out), _stream(stream)))
     return out
 

@@ -1,0 +1,132 @@
+// nm_act.cuh -- activations of the fused output stages, in fp32, and the packed
+// pairs of fp32 values they are computed on.
+//
+// The GELU is the erf form x/2 (1 + erf(x / sqrt 2)), with erf evaluated by
+// Abramowitz and Stegun's formula 7.1.26 (Handbook of Mathematical Functions,
+// after Hastings): for u >= 0,
+//   erfc(u) = (a1 t + a2 t^2 + a3 t^3 + a4 t^4 + a5 t^5) exp(-u^2) + e(u),
+//   t = 1 / (1 + p u),  |e(u)| <= 1.5e-7,
+// so that, with q = erfc(|x| / sqrt 2) / 2, GELU(x) = x (1 - q) for x >= 0 and
+// x q for x < 0.  The reciprocal and the power of two are the hardware's
+// approximate instructions (about 1 and 2 ulp); the whole function stays within
+// |y - GELU(x)| <= 4e-7 |x| + 2e-6 |GELU(x)| of the exact value (checked by a
+// dense sweep against fp64 in the tests).  Pairs of values go through the
+// packed fp32 pipe (add/mul/fma .f32x2: each half is its own fp32 operation,
+// rounded to nearest even), which halves the instruction count of the
+// arithmetic; a single value takes the same operations in the same order, so
+// both give identical results.
+#pragma once
+#include <cstdint>
+
+#include "nm_device.cuh"
+
+namespace nm {
+
+namespace gelu_as {
+constexpr float kP = 0.2316418883f;     // p / sqrt 2, p = 0.3275911
+constexpr float kB1 = 0.127414796f;     // a_i / 2
+constexpr float kB2 = -0.142248368f;
+constexpr float kB3 = 0.7107068705f;
+constexpr float kB4 = -0.7265760135f;
+constexpr float kB5 = 0.5307027145f;
+constexpr float kE = -0.7213475204f;    // -log2(e) / 2: exp(-x^2 / 2) = 2^(kE x^2)
+}  // namespace gelu_as
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float ex2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Two fp32 values in one 64-bit register pair, and the packed operations on them.
+__device__ __forceinline__ uint64_t pk2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void upk2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+__device__ __forceinline__ float gelu1(float x) {
+  using namespace gelu_as;
+  const float ax = fabsf(x);
+  const float t = rcp_approx(__fmaf_rn(ax, kP, 1.0f));
+  float h = __fmaf_rn(t, kB5, kB4);
+  h = __fmaf_rn(t, h, kB3);
+  h = __fmaf_rn(t, h, kB2);
+  h = __fmaf_rn(t, h, kB1);
+  h = __fmul_rn(t, h);
+  const float e = ex2_approx(__fmul_rn(x, __fmul_rn(x, kE)));
+  const float q = __fmul_rn(h, e);
+  return __fmul_rn(x, x >= 0.0f ? __fsub_rn(1.0f, q) : q);
+}
+
+// gelu1 of both halves of a pair.
+__device__ __forceinline__ void gelu2(float& x0, float& x1) {
+  using namespace gelu_as;
+  const uint64_t x = pk2(x0, x1);
+  const uint64_t d = fma2(pk2(fabsf(x0), fabsf(x1)), pk2(kP, kP), pk2(1.0f, 1.0f));
+  float d0, d1;
+  upk2(d, d0, d1);
+  const uint64_t t = pk2(rcp_approx(d0), rcp_approx(d1));
+  uint64_t h = fma2(t, pk2(kB5, kB5), pk2(kB4, kB4));
+  h = fma2(t, h, pk2(kB3, kB3));
+  h = fma2(t, h, pk2(kB2, kB2));
+  h = fma2(t, h, pk2(kB1, kB1));
+  h = mul2(t, h);
+  float w0, w1;
+  upk2(mul2(x, mul2(x, pk2(kE, kE))), w0, w1);
+  float q0, q1;
+  upk2(mul2(h, pk2(ex2_approx(w0), ex2_approx(w1))), q0, q1);
+  float r0, r1;  // 1 - q (x >= 0) or q (x < 0)
+  upk2(add2(pk2(1.0f, 1.0f), pk2(-q0, -q1)), r0, r1);
+  upk2(mul2(x, pk2(x0 >= 0.0f ? r0 : q0, x1 >= 0.0f ? r1 : q1)), x0, x1);
+}
+
+// SiLU(x) = x / (1 + exp(-x)) with the approximate power of two and reciprocal:
+// exp(-x) to 2 ulp plus the rounding of x log2(e) (1.2e-7 |x| relative), the
+// reciprocal to 1 ulp; a power that overflows gives 0, one that vanishes gives x.
+constexpr float kLog2e = 1.4426950409f;
+__device__ __forceinline__ float sigmoid1(float x) { return rcp_approx(__fadd_rn(1.0f, ex2_approx(__fmul_rn(x, -kLog2e)))); }
+__device__ __forceinline__ float silu1(float x) { return __fmul_rn(x, sigmoid1(x)); }
+// max(x, 0) that lets a NaN through.
+__device__ __forceinline__ float relu1(float x) { return x < 0.0f ? 0.0f : x; }
+
+// act(x) of N values, one uniform branch around each activation's loop.
+template <int N>
+__device__ __forceinline__ void act_run(float* x, int act) {
+  static_assert(N % 2 == 0, "values go in pairs");
+  if (act == ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) gelu2(x[i], x[i + 1]);
+  } else if (act == ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = silu1(x[i]);
+  } else if (act == ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = relu1(x[i]);
+  }
+}
+
+}  // namespace nm

@@ -19,12 +19,16 @@
 #include "nmspmm.h"
 #include "nm_device.cuh"
 #include "nm_internal.h"
+#include "nm_api_internal.h"
 
 namespace {
-
 thread_local std::string g_err;
+}
 
-nm_status fail(nm_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+namespace nm {
+
+void clear_error() { g_err.clear(); }
+
 nm_status fail(nm_status st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -39,8 +43,6 @@ nm_status cuda_fail(cudaError_t e, const char* what) {
   return fail(e == cudaErrorMemoryAllocation ? NM_ERR_OOM : NM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 int num_sms(int dev) {
   static int cache[64] = {0};
   if (dev < 0 || dev >= 64) return 148;
@@ -51,6 +53,30 @@ int num_sms(int dev) {
   }
   return cache[dev];
 }
+
+nm_status check_handle(const nm_handle* h) {
+  if (!h) return fail(NM_ERR_INVALID, "null handle");
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev != h->device)
+    return fail(NM_ERR_INVALID, "handle belongs to device %d but the current device is %d", h->device, dev);
+  return NM_OK;
+}
+
+bool pattern_supported(int N, int M, bool* sp24) {
+  *sp24 = (N == 1 && M == 4) || (N == 2 && M == 4) || (N == 2 && M == 8);
+  return *sp24 || (N == 4 && M == 8) || (N == M && (M == 4 || M == 8));
+}
+
+}  // namespace nm
+
+namespace {
+
+using nm::aligned;
+using nm::check_handle;
+using nm::cuda_fail;
+using nm::EpiReq;
+using nm::fail;
+using nm::num_sms;
 
 int env_int(const char* name, int dflt) {
   const char* v = getenv(name);
@@ -73,6 +99,33 @@ EncodeTiledFn encode_fn() {
   }
   return fn;
 }
+
+}  // namespace
+
+namespace nm {
+nm_status encode_map(CUtensorMap* map, CUtensorMapDataType ty, int rank, const void* base, const uint64_t* dims,
+                     const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle,
+                     CUtensorMapL2promotion promotion) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return fail(NM_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], es[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    es[i] = 1;
+    if (i + 1 < rank) st[i] = strides[i];
+  }
+  CUresult r = enc(map, ty, (cuuint32_t)rank, const_cast<void*>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   swizzle, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(NM_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for a tensor of %lld x %lld elements", (int)r,
+                (long long)dims[0], (long long)dims[1]);
+  return NM_OK;
+}
+}  // namespace nm
+
+namespace {
 
 // Activation X [T][k] as a 2-D tensor: inner dim k, box = 128 bytes x bn rows,
 // 128-byte swizzle (the layout the MMA's K-major B descriptor expects);
@@ -422,22 +475,6 @@ nm::Plan make_plan(const nm_handle* h, int64_t T, int sms, bool scaled) {
   return plan_with(h, T, sms, device_capacity(h, scaled));
 }
 
-nm_status check_handle(const nm_handle* h) {
-  if (!h) return fail(NM_ERR_INVALID, "null handle");
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev != h->device)
-    return fail(NM_ERR_INVALID, "handle belongs to device %d but the current device is %d", h->device, dev);
-  return NM_OK;
-}
-
-// Output stage chosen at run time (nm_spmm_ex); out_ty < 0: the fixed stage of nm_spmm.
-struct EpiReq {
-  int out_ty = -1;  // nm::OUT_F32 / F16 / BF16 / I8
-  const float* bias = nullptr;
-  int act = nm::ACT_NONE;
-  float out_scale = 1.0f;
-};
-
 int out_elem_bytes(const nm_handle* h, const EpiReq* ep) {
   if (ep && ep->out_ty >= 0)
     return ep->out_ty == nm::OUT_I8 ? 1 : (ep->out_ty == nm::OUT_F32 ? 4 : 2);
@@ -475,7 +512,10 @@ nm_status ensure_split_workspace(nm_handle* h, const nm::Plan& p) {
 // the runtime stage to run.
 nm_status resolve_epilogue(const nm_handle* h, const nm_epilogue* ep, bool* fixed, EpiReq* r) {
   if ((int)ep->out < 0 || (int)ep->out > 5) return fail(NM_ERR_INVALID, "unknown output type %d", (int)ep->out);
-  if ((int)ep->act < 0 || (int)ep->act > 1) return fail(NM_ERR_INVALID, "unknown activation %d", (int)ep->act);
+  if ((int)ep->act < 0 || (int)ep->act > (int)NM_ACT_RELU)
+    return fail(NM_ERR_INVALID, "unknown activation %d", (int)ep->act);
+  if (ep->act > NM_ACT_GELU)
+    return fail(NM_ERR_UNSUPPORTED, "activation %d is for gated products only", (int)ep->act);
   if ((ep->scale && !aligned(ep->scale, 4)) || (ep->bias && !aligned(ep->bias, 4)))
     return fail(NM_ERR_INVALID, "scale and bias must be 4-byte aligned");
   const bool plain = !ep->scale && !ep->bias && ep->act == NM_ACT_NONE;
@@ -501,6 +541,9 @@ nm_status resolve_epilogue(const nm_handle* h, const nm_epilogue* ep, bool* fixe
 }
 
 nm_status reject_tile(const nm_handle* h) {
+  if (h->mx)
+    return fail(NM_ERR_INVALID, "the handle was made by nm_compress_mx: its product is nm_spmm_mx%s",
+                h->gated ? "_gated" : "");
   if (h->tile) return fail(NM_ERR_INVALID, "the handle was made by nm_compress_tile: its product is nm_spmm_gather");
   return NM_OK;
 }
@@ -667,9 +710,8 @@ nm_status nm_compress(const void* W_dev, int64_t n_out, int64_t k, nm_dtype dt, 
   if (dt == NM_INT8 && k > (1 << 17))
     return fail(NM_ERR_UNSUPPORTED, "INT8 k is limited to 2^17 (int32 accumulation must not overflow)");
   if (M <= 0 || N <= 0 || N > M) return fail(NM_ERR_INVALID, "bad N:M %d:%d", N, M);
-  const bool sp24 = (N == 1 && M == 4) || (N == 2 && M == 4) || (N == 2 && M == 8);
-  const bool dense = (N == 4 && M == 8) || (N == M && (M == 4 || M == 8));
-  if (!sp24 && !dense) return fail(NM_ERR_UNSUPPORTED, "N:M %d:%d is not supported", N, M);
+  bool sp24 = false;
+  if (!nm::pattern_supported(N, M, &sp24)) return fail(NM_ERR_UNSUPPORTED, "N:M %d:%d is not supported", N, M);
   if (k % M != 0) return fail(NM_ERR_INVALID, "k=%lld is not a multiple of M=%d", (long long)k, M);
   const int es = nm::elem_bytes((int)dt);
   if (!aligned(W_dev, (size_t)es)) return fail(NM_ERR_INVALID, "W is not element aligned");
@@ -719,9 +761,11 @@ nm_status nm_recompress(nm_handle* h, const void* W_dev, void* stream) {
   nm_status st = check_handle(h);
   if (st != NM_OK) return st;
   if (!W_dev) return fail(NM_ERR_INVALID, "null W");
-  if (!aligned(W_dev, (size_t)nm::elem_bytes(h->dt))) return fail(NM_ERR_INVALID, "W is not element aligned");
-  cudaError_t e = h->tile ? nm::launch_compress_tile(h, W_dev, (cudaStream_t)stream)
-                          : nm::launch_compress(h, W_dev, (cudaStream_t)stream);
+  if (!aligned(W_dev, h->mx ? (size_t)16 : (size_t)nm::elem_bytes(h->dt)))
+    return fail(NM_ERR_INVALID, h->mx ? "W must be 16-byte aligned" : "W is not element aligned");
+  cudaError_t e = h->mx ? nm::launch_mx_pack(h, W_dev, (cudaStream_t)stream)
+                  : h->tile ? nm::launch_compress_tile(h, W_dev, (cudaStream_t)stream)
+                            : nm::launch_compress(h, W_dev, (cudaStream_t)stream);
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "launch compress kernel");
 }
 
@@ -842,7 +886,7 @@ namespace {
 nm_status gather_impl(const nm_handle* hc, const void* Xt, int64_t ldx, int64_t T, void* Y, const float* scale,
                       void* stream, const EpiReq* ep) {
   nm_status st = NM_OK;
-  if (!hc->tile) return fail(NM_ERR_INVALID, "nm_spmm_gather needs a handle made by nm_compress_tile");
+  if (!hc->tile || hc->mx) return fail(NM_ERR_INVALID, "nm_spmm_gather needs a handle made by nm_compress_tile");
   nm_handle* h = const_cast<nm_handle*>(hc);  // only caches (tensor map, workspace) change
   if (T < 0) return fail(NM_ERR_INVALID, "T must be >= 0 (got %lld)", (long long)T);
   if (T == 0) return NM_OK;
@@ -904,13 +948,15 @@ nm_status nm_decompress(const nm_handle* h, void* W_dev_out, void* stream) {
   if (st != NM_OK) return st;
   if (!W_dev_out) return fail(NM_ERR_INVALID, "null output");
   if (!aligned(W_dev_out, 16)) return fail(NM_ERR_INVALID, "output must be 16-byte aligned");
-  cudaError_t e = nm::launch_decompress(h, W_dev_out, (cudaStream_t)stream);
+  cudaError_t e = h->mx ? nm::launch_mx_unpack(h, W_dev_out, (cudaStream_t)stream)
+                        : nm::launch_decompress(h, W_dev_out, (cudaStream_t)stream);
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "launch decompress kernel");
 }
 
 nm_status nm_export_sizes(const nm_handle* h, size_t* values_bytes, size_t* idx_bytes) {
   g_err.clear();
   if (!h) return fail(NM_ERR_INVALID, "null handle");
+  if (h->mx) return fail(NM_ERR_INVALID, "the handle was made by nm_compress_mx: it has no canonical N:M format");
   if (values_bytes) *values_bytes = h->values_bytes;
   if (idx_bytes) *idx_bytes = h->idx_bytes;
   return NM_OK;
@@ -920,6 +966,7 @@ nm_status nm_export(const nm_handle* h, void* values_host, uint8_t* idx_host) {
   g_err.clear();
   nm_status st = check_handle(h);
   if (st != NM_OK) return st;
+  if (h->mx) return fail(NM_ERR_INVALID, "the handle was made by nm_compress_mx: it has no canonical N:M format");
   if (!values_host || !idx_host) return fail(NM_ERR_INVALID, "null host buffer");
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "synchronise before export");
@@ -935,6 +982,7 @@ nm_status nm_plan_query(const nm_handle* h, int64_t T, int scaled, nm_plan_info*
   nm_status st = check_handle(h);
   if (st != NM_OK) return st;
   if (!out) return fail(NM_ERR_INVALID, "null output");
+  if (h->mx) return fail(NM_ERR_INVALID, "the handle was made by nm_compress_mx: it has no N:M launch plan");
   if (T <= 0 || T > INT32_MAX) return fail(NM_ERR_INVALID, "T must be in [1, 2^31-1] (got %lld)", (long long)T);
   const nm::Plan p = make_plan(h, T, num_sms(h->device), scaled != 0);
   out->pair = p.pair;
@@ -952,9 +1000,8 @@ nm_status nm_plan_for_shape(nm_dtype dt, int64_t n_out, int64_t k, int N, int M,
   if (!pair_clusters || !stream_clusters || !out) return fail(NM_ERR_INVALID, "null argument");
   if (dt != NM_INT8 && dt != NM_FP16 && dt != NM_BF16) return fail(NM_ERR_INVALID, "unknown dtype %d", (int)dt);
   if (n_out <= 0 || k <= 0 || n_out > INT32_MAX || k > INT32_MAX) return fail(NM_ERR_INVALID, "bad shape");
-  const bool sp24 = (N == 1 && M == 4) || (N == 2 && M == 4) || (N == 2 && M == 8);
-  const bool dense = (N == 4 && M == 8) || (N == M && (M == 4 || M == 8));
-  if (!sp24 && !dense) return fail(NM_ERR_UNSUPPORTED, "N:M %d:%d is not supported", N, M);
+  bool sp24 = false;
+  if (!nm::pattern_supported(N, M, &sp24)) return fail(NM_ERR_UNSUPPORTED, "N:M %d:%d is not supported", N, M);
   if (k % M != 0) return fail(NM_ERR_INVALID, "k=%lld is not a multiple of M=%d", (long long)k, M);
   if (T <= 0 || T > INT32_MAX) return fail(NM_ERR_INVALID, "T must be in [1, 2^31-1] (got %lld)", (long long)T);
   if (sms <= 0) return fail(NM_ERR_INVALID, "sms must be positive");
@@ -1030,6 +1077,8 @@ void nm_destroy(nm_handle* h) {
   cudaFree(h->d_idx);
   cudaFree(h->d_bpack);
   cudaFree(h->d_kidx);
+  cudaFree(h->d_mxq);
+  cudaFree(h->d_mxs);
   cudaFree(h->d_err);
   cudaFree(h->d_ws);
   cudaFree(h->d_cnt);

@@ -42,7 +42,7 @@ namespace nm {
 enum : int { DT_I8 = 0, DT_F16 = 1, DT_BF16 = 2 };
 enum : int { IMG_SP24 = 0, IMG_DENSE = 1, IMG_GATHER = 2 };
 enum : int { OUT_I32 = 0, OUT_F32 = 1, OUT_F16 = 2, OUT_BF16 = 3, OUT_I8 = 4 };  // output element of a launch
-enum : int { ACT_NONE = 0, ACT_GELU = 1 };  // activation of the fused output stage
+enum : int { ACT_NONE = 0, ACT_GELU = 1, ACT_SILU = 2, ACT_RELU = 3 };  // activation of the fused output stage
 
 constexpr int kRows = 128;          // channel rows per tile (MMA M)
 constexpr int kAtomBytes = 16384;   // 128 rows x 128 B swizzled atom
@@ -69,6 +69,22 @@ __host__ __device__ inline uint32_t meta_off16(int dt, uint32_t r, uint32_t kk) 
   const uint32_t k1 = (kk >> 4) & 1u, k2 = kk >> 5;
   const uint32_t line = m0 + 8u * k1 + 16u * m2;
   return line * 16u + 4u * k2 + 2u * m1;
+}
+
+// Row of W [2 n_ff][k] that a gated handle's packed row r holds: groups of 32
+// packed rows are 16 gate rows, then the 16 up rows of the same channels.
+// -1: padding (a channel at or beyond n_ff).
+__host__ __device__ inline int64_t gated_source_row(int64_t r, int64_t n_ff) {
+  const int64_t ch = (r >> 5) * 16 + (r & 15);
+  return ch >= n_ff ? -1 : ((r & 16) ? n_ff + ch : ch);
+}
+__host__ __device__ inline int64_t gated_packed_rows(int64_t n_ff) { return (n_ff + 15) / 16 * 32; }
+
+// Offset of the scale byte of (row r, 32-block b) in microscaled scale tiles
+// (128 rows x 256 k each, n_kb tiles along k): in the tensor core's order, 32
+// lanes x 16 bytes, where byte 4 q + i of lane l is row 32 q + l, block i of four.
+__host__ __device__ inline int64_t mx_scale_offset(int64_t r, int64_t b, int64_t n_kb) {
+  return ((r >> 7) * n_kb + (b >> 3)) * 1024 + ((b >> 2) & 1) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
 }
 
 // ------------------------------------------------------------------ PTX wrappers
@@ -365,6 +381,13 @@ __device__ __forceinline__ void tc_cp_128x128b_pair(uint32_t taddr, uint64_t sde
   asm volatile("tcgen05.cp.cta_group::2.128x128b [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
+// 512 bytes (32 lanes x 16 bytes, lane rows 16 B apart) into four columns, the
+// 32 lanes repeated for the four lane quarters; both CTAs of a pair, each from
+// its own shared memory.  The layout of block scale factors.
+__device__ __forceinline__ void tc_cp_32x128b_x4_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
 template <int KIND>  // 0: kind::i8, 1: kind::f16
 __device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -436,6 +459,17 @@ __device__ __forceinline__ void tc_mma_sp_pair(uint32_t d_tmem, uint64_t adesc, 
         : "memory");
   }
 }
+// CTA-pair MMA of two 4-bit operands with one E8M0 scale per 32 k of each row
+// (K = 64: two scale bytes per row, chosen by the data ids in idesc).
+__device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                 uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      : "memory");
+}
 // Pair leader: arrive on the mbarrier at this shared-memory offset in every CTA
 // of `cta_mask` once all prior tcgen05 operations of this thread complete.
 __device__ __forceinline__ void tc_commit_pair(uint64_t* bar, uint16_t cta_mask) {
@@ -457,6 +491,19 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* smem_src, int c0, int c1) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
                "r"(smem_u32(smem_src)), "r"(c0), "r"(c1)
+               : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map, uint32_t bar_cluster_addr,
+                                                 int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(map), "r"(bar_cluster_addr), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+               "r"(smem_u32(smem_src)), "r"(c0), "r"(c1), "r"(c2)
                : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }

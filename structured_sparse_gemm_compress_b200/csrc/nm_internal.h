@@ -7,6 +7,8 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "nm_device.cuh"
+
 struct nm_handle {
   int64_t n_out = 0, k = 0;
   int N = 0, M = 0;
@@ -31,6 +33,21 @@ struct nm_handle {
   int32_t* d_kidx = nullptr;
   size_t kidx_bytes = 0;
   int* d_err = nullptr;       // device error word (bounded-wait timeouts)
+
+  // two projections of a gated block: rows [0, n_out / 2) gate, the rest up;
+  // the packed image interleaves them 16 by 16 (nm::gated_source_row)
+  int gated = 0;
+
+  // microscaled 4-bit weight (nm_compress_mx): codes [mx_rows][k / 2] and scale
+  // tiles; no canonical format and no packed image
+  int mx = 0;
+  int src_dt = 0;             // element type of the source weight (NM_FP32 / FP16 / BF16)
+  int64_t mx_rows = 0;        // rows of the code matrix (gated: whole 32-row groups)
+  uint8_t* d_mxq = nullptr;
+  uint8_t* d_mxs = nullptr;
+  size_t mxs_bytes = 0;
+  alignas(64) CUtensorMap tm_mxq[3];  // codes, one box height per channel tile of the product
+  alignas(64) CUtensorMap tm_mxs;     // scale tiles as rows of 128 bytes
 
   // split-K workspace (partials + per-tile arrival counters), grown on demand
   void* d_ws = nullptr;
@@ -128,6 +145,9 @@ constexpr int kTraceStride = TR_KINDS * kTraceMax;
 
 cudaError_t launch_compress(const nm_handle* h, const void* W, cudaStream_t s);
 cudaError_t launch_decompress(const nm_handle* h, void* Wout, cudaStream_t s);
+// Microscaled weights (nm_compress_mx): quantise into the handle; the values back as BF16.
+cudaError_t launch_mx_pack(const nm_handle* h, const void* W, cudaStream_t s);
+cudaError_t launch_mx_unpack(const nm_handle* h, void* W, cudaStream_t s);
 // Tile-shared compress (nm_compress_tile): selects each tile's kept k, then packs.
 cudaError_t launch_compress_tile(const nm_handle* h, const void* W, cudaStream_t s);
 // Resident CTA pairs for the pair kernel of this (dtype, image, token tile, output) or <= 0.
