@@ -277,6 +277,71 @@ nm_status nm_spmm_gather_ex(const nm_handle* h, const void* Xt_dev, int64_t ldx,
                             const nm_epilogue* ep, void* stream);
 
 /*
+ * Gated feed-forward block.  (No counterpart in the paper, whose feed-forward
+ * linears are ungated: it is the same N:M product with a gated output stage.)
+ *
+ * nm_compress_gated -- prune and pack the two projections of a gated block.
+ * W_dev [2 n_ff][k] holds the n_ff rows of the gate projection, then the n_ff
+ * rows of the up projection.  Pruning, formats, limits and errors are those of
+ * nm_compress for the [2 n_ff][k] weight; the packed image interleaves 16 gate
+ * rows with their 16 up rows so that one accumulator tile holds both.
+ * nm_recompress, nm_decompress, nm_export and nm_query (n_out = 2 n_ff) accept
+ * the handle and see W's own row order; the ungated products reject it.
+ */
+nm_status nm_compress_gated(const void* W_dev, int64_t n_ff, int64_t k, nm_dtype dt, int N, int M, void* stream,
+                            nm_handle** out);
+
+/*
+ * nm_spmm_gated -- both projections, the activation and the product in one
+ * kernel:
+ *   p[t][r] = acc(X . Wm^T)[t][r] * scale[r] + bias[r]      r in [0, 2 n_ff)
+ *   Y[t][f] = act(p[t][f]) * p[t][n_ff + f]                 f in [0, n_ff)
+ * in fp32, each step rounded to nearest as in nm_spmm_ex, Y rounded once to its
+ * type.  act is any nm_act.  ep->scale and ep->bias are [2 n_ff] (or NULL);
+ * output types, errors and defaults are nm_spmm_ex's, but NM_OUT_INT32 is
+ * refused, and the default of an INT8 handle is fp32.  ep == NULL: NM_ACT_SILU,
+ * default output.  The SiLU is within (6e-7 + 1.3e-7 max(0, -v)) |SiLU(v)| +
+ * 1e-36 of the exact one.
+ *
+ * P_dev, if not NULL, receives p itself, [T][2 n_ff] in the handle's type
+ * (FP16/BF16; an INT8 handle refuses it with NM_ERR_UNSUPPORTED): what
+ * nm_gated_backward needs.  16-byte aligned, overlapping neither X nor Y.
+ * X, T, alignment and streams as nm_spmm.  Never allocates or synchronises and
+ * keeps nothing between calls: calls on one handle may overlap.
+ */
+nm_status nm_spmm_gated(const nm_handle* h, const void* X_dev, int64_t T, void* Y_dev, void* P_dev,
+                        const nm_epilogue* ep, void* stream);
+
+/*
+ * nm_gated_backward -- gradients of the gated block of an FP16 or BF16 handle
+ * (made by nm_compress_gated; INT8: NM_ERR_UNSUPPORTED).  With g, u the two
+ * halves of p (as nm_spmm_gated saved it, computed without a scale):
+ *   dp[t][f]        = dY[t][f] * u * act'(g)      (RELU: act'(0) = 0)
+ *   dp[t][n_ff + f] = dY[t][f] * act(g)
+ *   dX [T][k]       = dp . Wm
+ *   dW [2 n_ff][k]  = dp^T . X      the gradient of Wm at every position; a
+ *                     pruned weight's own gradient is zero (mask it), while
+ *                     straight-through training uses all of it
+ *   dbias [2 n_ff]  = sum over t of dp, fp32
+ * dX and dW have the handle's type.  dp is computed in fp32; the two products
+ * read it rounded to the handle's type (their tensor-core operand), sum in fp32
+ * and round once; dbias sums the unrounded fp32 values, in a fixed order.
+ * Results do not depend on timing.
+ *
+ * dX_dev, dW_dev, dbias_dev: any may be NULL (not computed), not all three.
+ * X_dev [T][k] (needed for dW only, else may be NULL), P_dev [T][2 n_ff],
+ * dY_dev [T][n_ff], all in the handle's type, all pointers 16-byte aligned;
+ * k a multiple of 8 (else NM_ERR_UNSUPPORTED).  T == 0 writes zeros to dW and
+ * dbias.  ws_dev: device workspace of at least nm_gated_backward_workspace
+ * bytes, 16-byte aligned, for this call alone until it has run; calls that
+ * overlap need one each.  Outputs and workspace overlap nothing else.
+ */
+nm_status nm_gated_backward_workspace(const nm_handle* h, int64_t T, size_t* bytes);
+nm_status nm_gated_backward(const nm_handle* h, const void* X_dev, const void* P_dev, const void* dY_dev, int64_t T,
+                            nm_act act, void* dX_dev, void* dW_dev, float* dbias_dev, void* ws_dev, size_t ws_bytes,
+                            void* stream);
+
+/*
  * Microscaled 4-bit floating point (the MXFP4 format of the OCP Microscaling
  * Formats specification, version 1.0).  (No counterpart in the paper: it is a
  * further storage format for the same linears.)  Along k, every block of 32

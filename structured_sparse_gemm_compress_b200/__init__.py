@@ -29,7 +29,8 @@ EXPORTS = ("nm_compress", "nm_compress_tile", "nm_recompress", "nm_spmm", "nm_sp
            "nm_spmm_gather_ex", "nm_spmm_noalloc", "nm_decompress", "nm_export", "nm_export_sizes", "nm_query",
            "nm_plan_query", "nm_plan_for_shape", "nm_device_status", "nm_destroy", "nm_last_error", "nm_version",
            "nm_test_spmm_skip_stage", "nm_mx_scale_bytes", "nm_mx_quantize", "nm_mx_dequantize", "nm_compress_mx",
-           "nm_spmm_mx", "nm_spmm_mx_gated")
+           "nm_spmm_mx", "nm_spmm_mx_gated", "nm_compress_gated", "nm_spmm_gated", "nm_gated_backward",
+           "nm_gated_backward_workspace")
 
 
 class NMPlanInfo(ctypes.Structure):
@@ -79,6 +80,10 @@ def lib() -> ctypes.CDLL:
         L.nm_compress_mx.argtypes = [vp, i64, i64, i32, i32, i32, i32, vp, ctypes.POINTER(vp)]
         L.nm_spmm_mx.argtypes = [vp, vp, vp, i64, vp, ctypes.POINTER(NMEpilogue), vp]
         L.nm_spmm_mx_gated.argtypes = [vp, vp, vp, i64, vp, ctypes.POINTER(NMEpilogue), vp]
+        L.nm_compress_gated.argtypes = [vp, i64, i64, i32, i32, i32, vp, ctypes.POINTER(vp)]
+        L.nm_spmm_gated.argtypes = [vp, vp, i64, vp, vp, ctypes.POINTER(NMEpilogue), vp]
+        L.nm_gated_backward_workspace.argtypes = [vp, i64, ctypes.POINTER(ctypes.c_size_t)]
+        L.nm_gated_backward.argtypes = [vp, vp, vp, vp, i64, i32, vp, vp, vp, vp, ctypes.c_size_t, vp]
         L.nm_device_status.argtypes = [vp]
         L.nm_destroy.argtypes = [vp]
         L.nm_destroy.restype = None
@@ -88,7 +93,8 @@ def lib() -> ctypes.CDLL:
                      "nm_spmm_gather_ex", "nm_spmm_noalloc",
                      "nm_test_spmm_skip_stage", "nm_decompress", "nm_export", "nm_export_sizes", "nm_query",
                      "nm_plan_query", "nm_plan_for_shape", "nm_device_status", "nm_mx_scale_bytes", "nm_mx_quantize",
-                     "nm_mx_dequantize", "nm_compress_mx", "nm_spmm_mx", "nm_spmm_mx_gated"):
+                     "nm_mx_dequantize", "nm_compress_mx", "nm_spmm_mx", "nm_spmm_mx_gated",
+                     "nm_compress_gated", "nm_spmm_gated", "nm_gated_backward", "nm_gated_backward_workspace"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -125,7 +131,7 @@ def _check_tensor(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) 
     """A contiguous tensor of this type and shape on the current CUDA device."""
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor")
-    if t.get_device() != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} must be on the current CUDA device")
 
 
@@ -322,6 +328,83 @@ def _epilogue(h: NMHandle, scale, bias, act: str, out: str, out_scale: float) ->
     return NMEpilogue(OUT_TYPES[out], ACTS[act], _ptr(scale), _ptr(bias), float(out_scale))
 
 
+def nm_compress_gated(W: torch.Tensor, N: int, M: int, stream=None) -> NMHandle:
+    """Prune and pack the two projections of a gated block: W [2 n_ff, k] (int8 /
+    fp16 / bf16), the gate rows first, for ``nm_spmm_gated``."""
+    if W.dim() != 2 or W.dtype not in _TORCH_DT or W.shape[0] % 2:
+        raise ValueError("W must be a [2 n_ff, k] int8/float16/bfloat16 tensor")
+    _check_tensor("W", W, W.dtype, tuple(W.shape))
+    n_out, k = W.shape
+    out = ctypes.c_void_p()
+    _check(lib().nm_compress_gated(W.data_ptr(), n_out // 2, k, _TORCH_DT[W.dtype], N, M, _stream(stream),
+                                   ctypes.byref(out)))
+    return NMHandle(out.value, n_out, k, N, M, _TORCH_DT[W.dtype], gated=True)
+
+
+def nm_spmm_gated(h: NMHandle, X: torch.Tensor, Y: torch.Tensor | None = None, P: torch.Tensor | None = None,
+                  scale: torch.Tensor | None = None, bias: torch.Tensor | None = None, act: str = "silu",
+                  out: str = "default", out_scale: float = 1.0, stream=None) -> torch.Tensor:
+    """Y [T, n_ff] = act(g) * u with g, u the halves of X @ Wm^T * scale + bias, in
+    one kernel.  P [T, 2 n_ff] (the handle's type), if given, receives g and u for
+    ``nm_gated_backward``."""
+    if X.dim() != 2:
+        raise ValueError("X must be [T, k]")
+    T, n = X.shape[0], h.n_out // 2
+    _check_tensor("X", X, h.dtype, (T, h.k))
+    ep = _epilogue(h, scale, bias, act, out, out_scale)
+    want = (torch.float32 if h.dt == NM_INT8 else h.dtype) if out == "default" else _OUT_TORCH[out]
+    if Y is None:
+        Y = _empty((T, n), want, X.device, stream)
+    else:
+        _check_tensor("Y", Y, want, (T, n))
+    if P is not None:
+        _check_tensor("P", P, h.dtype, (T, h.n_out))
+    _check(lib().nm_spmm_gated(h.raw, X.data_ptr(), T, Y.data_ptr(), _ptr(P), ctypes.byref(ep), _stream(stream)))
+    return Y
+
+
+def nm_gated_backward_workspace(h: NMHandle, T: int) -> int:
+    """Bytes of device workspace one ``nm_gated_backward`` call for T tokens needs."""
+    n = ctypes.c_size_t()
+    _check(lib().nm_gated_backward_workspace(h.raw, int(T), ctypes.byref(n)))
+    return n.value
+
+
+def nm_gated_backward(h: NMHandle, X: torch.Tensor, P: torch.Tensor, dY: torch.Tensor, act: str = "silu",
+                      bias_grad: bool = False, dX: torch.Tensor | None = None, dW: torch.Tensor | None = None,
+                      dbias: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of ``nm_spmm_gated`` (fp16 / bf16 handles): (dX [T, k], dW [2 n_ff,
+    k], dbias [2 n_ff] fp32 or None).  dW is the gradient of the masked weight at
+    every position.  ``workspace``: a uint8 CUDA tensor, else one is allocated."""
+    if X.dim() != 2 or act not in ACTS:
+        raise ValueError(f"X must be [T, k], act one of {tuple(ACTS)}")
+    T, n = X.shape[0], h.n_out // 2
+    dt = h.dtype
+    _check_tensor("X", X, dt, (T, h.k))
+    _check_tensor("P", P, dt, (T, h.n_out))
+    _check_tensor("dY", dY, dt, (T, n))
+    if dX is None:
+        dX = _empty((T, h.k), dt, X.device, stream)
+    else:
+        _check_tensor("dX", dX, dt, (T, h.k))
+    if dW is None:
+        dW = _empty((h.n_out, h.k), dt, X.device, stream)
+    else:
+        _check_tensor("dW", dW, dt, (h.n_out, h.k))
+    if dbias is not None:
+        _check_tensor("dbias", dbias, torch.float32, (h.n_out,))
+    elif bias_grad:
+        dbias = _empty((h.n_out,), torch.float32, X.device, stream)
+    if workspace is None:
+        workspace = _empty((nm_gated_backward_workspace(h, T),), torch.uint8, X.device, stream)
+    else:
+        _check_tensor("workspace", workspace, torch.uint8, (workspace.numel(),))
+    _check(lib().nm_gated_backward(h.raw, X.data_ptr(), P.data_ptr(), dY.data_ptr(), T, ACTS[act], dX.data_ptr(),
+                                   dW.data_ptr(), _ptr(dbias), workspace.data_ptr(), workspace.numel(),
+                                   _stream(stream)))
+    return dX, dW, dbias
+
+
 def nm_mx_scale_bytes(rows: int, k: int) -> int:
     """Bytes of the scales of a microscaled [rows, k] matrix (layout in include/nmspmm.h)."""
     n = ctypes.c_size_t()
@@ -335,7 +418,7 @@ def nm_mx_quantize(X: torch.Tensor, Q: torch.Tensor | None = None, S: torch.Tens
     multiple of 16 bytes) to microscaled 4-bit codes Q [T, k / 2] and scales S (uint8)."""
     if X.dim() != 2 or X.dtype not in _MX_DT or (X.shape[1] > 1 and X.stride(1) != 1):
         raise ValueError("X must be a [T, k] float32/float16/bfloat16 tensor with contiguous rows")
-    if X.get_device() != torch.cuda.current_device():
+    if not X.is_cuda or X.get_device() != torch.cuda.current_device():
         raise ValueError("X must be on the current CUDA device")
     T, k = X.shape
     n = (T + 127) // 128 * ((k + 255) // 256) * 1024

@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libnmspmm.so")
 TRACE_LIB = os.path.join(PKG, "libnmspmm_trace.so")
 OBJDIR = os.path.join(PKG, "_build")
 TRACE_OBJDIR = os.path.join(PKG, "_build_trace")
-SOURCES = ["nm_api.cu", "nm_pack.cu", "nm_spmm.cu", "nm_mx.cu"]
+SOURCES = ["nm_api.cu", "nm_pack.cu", "nm_spmm.cu", "nm_gated.cu", "nm_grad.cu", "nm_mx.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-std=c++17", "-lineinfo",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall", "-I", INCLUDE, "-I", CSRC]

@@ -129,4 +129,35 @@ __device__ __forceinline__ void act_run(float* x, int act) {
   }
 }
 
+// a = act(x) and d = act'(x) (relu: 0 at 0).  GELU: with Phi the normal
+// distribution function (formula 7.1.26 as above) and phi its density,
+// a = x Phi(x), d = Phi(x) + x phi(x); both share the power of two.
+constexpr float kInvSqrt2Pi = 0.3989422804f;
+__device__ __forceinline__ void act_slope(float x, int act, float& a, float& d) {
+  if (act == ACT_GELU) {
+    using namespace gelu_as;
+    const float t = rcp_approx(__fmaf_rn(fabsf(x), kP, 1.0f));
+    float h = __fmaf_rn(t, kB5, kB4);
+    h = __fmaf_rn(t, h, kB3);
+    h = __fmaf_rn(t, h, kB2);
+    h = __fmaf_rn(t, h, kB1);
+    h = __fmul_rn(t, h);
+    const float e = ex2_approx(__fmul_rn(x, __fmul_rn(x, kE)));
+    const float q = __fmul_rn(h, e);
+    const float cdf = x >= 0.0f ? __fsub_rn(1.0f, q) : q;
+    a = __fmul_rn(x, cdf);
+    d = __fmaf_rn(x, __fmul_rn(kInvSqrt2Pi, e), cdf);
+  } else if (act == ACT_SILU) {
+    const float s = sigmoid1(x);
+    a = __fmul_rn(x, s);
+    d = __fmul_rn(s, __fmaf_rn(x, __fsub_rn(1.0f, s), 1.0f));
+  } else if (act == ACT_RELU) {
+    a = relu1(x);
+    d = x > 0.0f ? 1.0f : 0.0f;
+  } else {
+    a = x;
+    d = 1.0f;
+  }
+}
+
 }  // namespace nm

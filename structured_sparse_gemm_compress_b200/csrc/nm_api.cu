@@ -409,7 +409,7 @@ nm::Plan plan_with(const nm_handle* h, int64_t T, int sms, const Capacity& capac
   // sharing each X tile, and enough 128-token tiles to fill the SMs without split-K.
   const int64_t tt128 = (T + 127) / 128;
   const bool xs_ok = h->dt == nm::DT_I8 && h->n_kb <= nm::kXsMaxKb && (forced_bn == 0 || forced_bn == 128) &&
-                     forced_split <= 1 && h->n_ct >= 2;
+                     forced_split <= 1 && h->n_ct >= 2 && !h->gated;
   if (xs_ok && forced_xs == 1) {  // measured slower than streaming by default: its write order is scattered
     p.bn = 128;
     p.xkb = h->n_kb;
@@ -540,10 +540,12 @@ nm_status resolve_epilogue(const nm_handle* h, const nm_epilogue* ep, bool* fixe
   return NM_OK;
 }
 
-nm_status reject_tile(const nm_handle* h) {
+nm_status reject_other_kinds(const nm_handle* h) {
   if (h->mx)
     return fail(NM_ERR_INVALID, "the handle was made by nm_compress_mx: its product is nm_spmm_mx%s",
                 h->gated ? "_gated" : "");
+  if (h->gated)
+    return fail(NM_ERR_INVALID, "the handle was made by nm_compress_gated: its product is nm_spmm_gated");
   if (h->tile) return fail(NM_ERR_INVALID, "the handle was made by nm_compress_tile: its product is nm_spmm_gather");
   return NM_OK;
 }
@@ -589,7 +591,7 @@ nm_status spmm_impl(const nm_handle* hc, const void* X, int64_t T, void* Y, cons
   g_err.clear();
   nm_status st = check_handle(hc);
   if (st != NM_OK) return st;
-  if ((st = reject_tile(hc)) != NM_OK) return st;
+  if ((st = reject_other_kinds(hc)) != NM_OK) return st;
   nm_handle* h = const_cast<nm_handle*>(hc);  // only caches (tensor map, workspace) change
   if (T < 0) return fail(NM_ERR_INVALID, "T must be >= 0 (got %lld)", (long long)T);
   if (T == 0) return NM_OK;
@@ -691,6 +693,52 @@ nm_status gather_impl(const nm_handle* hc, const void* Xt, int64_t ldx, int64_t 
 
 }  // namespace
 
+namespace {
+
+// nm_compress and nm_compress_gated: n_out rows of W; gated: the first half gate,
+// the second half up, packed 16 by 16.
+nm_status compress_rows(const void* W_dev, int64_t n_out, int64_t k, nm_dtype dt, int N, int M, bool gated,
+                        void* stream, nm_handle** out);
+
+// X [T][k] as the K-major operand (make_x_map), into a map of the call's own.
+nm_status x_map(CUtensorMap* m, const nm_handle* h, const void* X, int64_t T, int bn) {
+  const int es = nm::elem_bytes(h->dt);
+  const uint64_t dims[2] = {(uint64_t)h->k, (uint64_t)T}, strides[1] = {(uint64_t)(h->k * es)};
+  const uint32_t box[2] = {(uint32_t)(128 / es), (uint32_t)bn};
+  return nm::encode_map(m,
+                        h->dt == nm::DT_I8    ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                        : h->dt == nm::DT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        2, X, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+// Validates the output stage of a gated product.
+nm_status resolve_gated(const nm_handle* h, const nm_epilogue* ep, EpiReq* r) {
+  const nm_epilogue dflt = {NM_OUT_DEFAULT, NM_ACT_SILU, nullptr, nullptr, 1.0f};
+  if (!ep) ep = &dflt;
+  if ((int)ep->out < 0 || (int)ep->out > 5) return fail(NM_ERR_INVALID, "unknown output type %d", (int)ep->out);
+  if ((int)ep->act < 0 || (int)ep->act > (int)NM_ACT_RELU)
+    return fail(NM_ERR_INVALID, "unknown activation %d", (int)ep->act);
+  if ((ep->scale && !aligned(ep->scale, 4)) || (ep->bias && !aligned(ep->bias, 4)))
+    return fail(NM_ERR_INVALID, "scale and bias must be 4-byte aligned");
+  nm_out_type out = ep->out;
+  if (out == NM_OUT_DEFAULT)
+    out = h->dt == nm::DT_I8 ? NM_OUT_FP32 : h->dt == nm::DT_F16 ? NM_OUT_FP16 : NM_OUT_BF16;
+  if (out == NM_OUT_INT32) return fail(NM_ERR_INVALID, "a gated product has no raw accumulator output");
+  if (out == NM_OUT_INT8 && h->dt != nm::DT_I8)
+    return fail(NM_ERR_UNSUPPORTED, "integer outputs need an INT8 handle");
+  if (out == NM_OUT_INT8 && !(std::isfinite(ep->out_scale) && ep->out_scale > 0.0f))
+    return fail(NM_ERR_INVALID, "out_scale must be finite and positive for NM_OUT_INT8");
+  r->out_ty = out == NM_OUT_FP32 ? nm::OUT_F32 : out == NM_OUT_FP16 ? nm::OUT_F16 : out == NM_OUT_BF16 ? nm::OUT_BF16
+                                                                                                       : nm::OUT_I8;
+  r->bias = ep->bias;
+  r->act = (int)ep->act;
+  r->out_scale = ep->out_scale;
+  return NM_OK;
+}
+
+}  // namespace
+
 extern "C" {
 
 const char* nm_last_error(void) { return g_err.c_str(); }
@@ -699,61 +747,71 @@ const char* nm_version(void) { return "nmspmm 0.1.0 (sm_100a)"; }
 
 nm_status nm_compress(const void* W_dev, int64_t n_out, int64_t k, nm_dtype dt, int N, int M, void* stream,
                       nm_handle** out) {
+  return compress_rows(W_dev, n_out, k, dt, N, M, false, stream, out);
+}
+
+nm_status nm_compress_gated(const void* W_dev, int64_t n_ff, int64_t k, nm_dtype dt, int N, int M, void* stream,
+                            nm_handle** out) {
+  const int64_t rows = (n_ff < 0 || n_ff > (1 << 24)) ? n_ff : 2 * n_ff;  // refused as it is, or doubled
+  return compress_rows(W_dev, rows, k, dt, N, M, true, stream, out);
+}
+
+nm_status nm_spmm_gated(const nm_handle* h, const void* X, int64_t T, void* Y, void* P, const nm_epilogue* ep,
+                        void* stream) {
   g_err.clear();
-  if (!out) return fail(NM_ERR_INVALID, "null output handle pointer");
-  *out = nullptr;
-  if (!W_dev) return fail(NM_ERR_INVALID, "null W");
-  if ((int)dt < 0 || (int)dt > 2) return fail(NM_ERR_INVALID, "unknown dtype %d", (int)dt);
-  if (n_out <= 0 || k <= 0) return fail(NM_ERR_INVALID, "n_out and k must be positive");
-  if (n_out > (1 << 24) || k > (1 << 24)) return fail(NM_ERR_UNSUPPORTED, "n_out and k are limited to 2^24");
-  // INT8 accumulates exactly in int32: |acc| <= k * 128 * 127 must stay below 2^31.
-  if (dt == NM_INT8 && k > (1 << 17))
-    return fail(NM_ERR_UNSUPPORTED, "INT8 k is limited to 2^17 (int32 accumulation must not overflow)");
-  if (M <= 0 || N <= 0 || N > M) return fail(NM_ERR_INVALID, "bad N:M %d:%d", N, M);
-  bool sp24 = false;
-  if (!nm::pattern_supported(N, M, &sp24)) return fail(NM_ERR_UNSUPPORTED, "N:M %d:%d is not supported", N, M);
-  if (k % M != 0) return fail(NM_ERR_INVALID, "k=%lld is not a multiple of M=%d", (long long)k, M);
-  const int es = nm::elem_bytes((int)dt);
-  if (!aligned(W_dev, (size_t)es)) return fail(NM_ERR_INVALID, "W is not element aligned");
+  nm_status st = check_handle(h);
+  if (st != NM_OK) return st;
+  if (!h->gated || h->mx) return fail(NM_ERR_INVALID, "nm_spmm_gated needs a handle made by nm_compress_gated");
+  EpiReq r;
+  if ((st = resolve_gated(h, ep, &r)) != NM_OK) return st;
+  if (P && h->dt == nm::DT_I8)
+    return fail(NM_ERR_UNSUPPORTED, "the pre-activations are saved for FP16 and BF16 handles only");
+  if (T < 0) return fail(NM_ERR_INVALID, "T must be >= 0 (got %lld)", (long long)T);
+  if (T == 0) return NM_OK;
+  if (!X || !Y) return fail(NM_ERR_INVALID, "null X or Y");
+  if (T > INT32_MAX) return fail(NM_ERR_UNSUPPORTED, "T above 2^31-1");
+  const int es = nm::elem_bytes(h->dt);
+  if (!aligned(X, 16) || !aligned(Y, 16) || !aligned(P, 16))
+    return fail(NM_ERR_INVALID, "X, Y and P must be 16-byte aligned");
+  if ((h->k * es) % 16 != 0)
+    return fail(NM_ERR_UNSUPPORTED, "k * sizeof(dtype) must be a multiple of 16 bytes (k=%lld)", (long long)h->k);
+  const size_t ybytes = (size_t)T * (h->n_out / 2) * out_elem_bytes(h, &r);
+  const size_t xbytes = (size_t)T * h->k * es, pbytes = P ? (size_t)T * h->n_out * es : 0;
+  if (nm::overlaps(X, xbytes, Y, ybytes) || (P && (nm::overlaps(X, xbytes, P, pbytes) ||
+                                                   nm::overlaps(Y, ybytes, P, pbytes))))
+    return fail(NM_ERR_INVALID, "X, Y and P overlap");
 
-  nm_handle* h = new (std::nothrow) nm_handle();
-  if (!h) return fail(NM_ERR_OOM, "host allocation failed");
-  cudaGetDevice(&h->device);
-  h->n_out = n_out;
-  h->k = k;
-  h->N = N;
-  h->M = M;
-  h->dt = (int)dt;
-  h->img = sp24 ? nm::IMG_SP24 : nm::IMG_DENSE;
-  const int KB = nm::kblock_elems(h->dt);
-  h->n_kb = (int)((k + KB - 1) / KB);
-  h->n_ct = (int)((n_out + nm::kRows - 1) / nm::kRows);
-  h->chunk = (size_t)nm::chunk_bytes(h->dt, h->img);
-  h->values_bytes = (size_t)n_out * (size_t)(k / M) * N * es;
-  h->idx_pitch = ((k / M) * N + 1) / 2;
-  h->idx_bytes = (size_t)n_out * (size_t)h->idx_pitch;
-  h->bpack_bytes = (size_t)h->n_ct * h->n_kb * h->chunk;
-
-  cudaError_t e;
-  nm_status st = NM_OK;
-  if ((e = cudaMalloc(&h->d_values, h->values_bytes)) != cudaSuccess) st = cuda_fail(e, "allocate values");
-  else if ((e = cudaMalloc(&h->d_idx, h->idx_bytes)) != cudaSuccess) st = cuda_fail(e, "allocate idx");
-  else if ((e = cudaMalloc(&h->d_bpack, h->bpack_bytes)) != cudaSuccess) st = cuda_fail(e, "allocate packed image");
-  else if ((e = cudaMalloc(&h->d_err, sizeof(int))) != cudaSuccess) st = cuda_fail(e, "allocate error word");
-  else if ((e = cudaMemsetAsync(h->d_err, 0, sizeof(int), (cudaStream_t)stream)) != cudaSuccess)
-    st = cuda_fail(e, "clear error word");
-  else if ((e = nm::launch_compress(h, W_dev, (cudaStream_t)stream)) != cudaSuccess)
-    st = cuda_fail(e, "launch compress kernel");
-  else
-    st = make_w_map(h);
-  if (st != NM_OK) {
-    const std::string msg = g_err;
-    nm_destroy(h);
-    g_err = msg;
-    return st;
-  }
-  *out = h;
-  return NM_OK;
+  const nm::Plan p = make_plan(h, T, num_sms(h->device), false);
+  if (p.splits > 1 && !p.cluster)
+    return fail(NM_ERR_UNSUPPORTED, "a gated product splits k on chip only (a global-memory split was forced)");
+  CUtensorMap tmX;
+  if ((st = x_map(&tmX, h, X, T, p.pair ? p.bn / 2 : p.bn)) != NM_OK) return st;
+  nm::SpmmArgs a{};
+  a.bpack = h->d_bpack;
+  a.Y = Y;
+  a.scale = ep ? ep->scale : nullptr;
+  a.err = h->d_err;
+  a.T = (int)T;
+  a.n_out = (int)h->n_out;
+  a.n_ff = (int)(h->n_out / 2);
+  a.P = P;
+  a.n_kb = h->n_kb;
+  a.n_ct = h->n_ct;
+  a.n_tt = p.n_tt;
+  a.splits = p.splits;
+  a.kb_per_split = p.kb_per_split;
+  a.units = p.units;
+  a.timeout_ns = 1000000000ull;
+  a.inject_skip = -1;
+  a.w_tma = (h->has_tmw && env_int("NMSPMM_W_BULK", 0) == 0) ? 1 : 0;
+  a.out_ty = r.out_ty;
+  a.bias = r.bias;
+  a.act = r.act;
+  a.out_scale = r.out_scale;
+  a.prefetch = std::max(0, std::min(2, env_int("NMSPMM_PREFETCH", 2)));
+  a.csplit = p.cluster;
+  cudaError_t e = nm::launch_spmm_gated(h, tmX, p, a, (cudaStream_t)stream);
+  return e == cudaSuccess ? NM_OK : cuda_fail(e, "launch the gated SpMM kernel");
 }
 
 nm_status nm_recompress(nm_handle* h, const void* W_dev, void* stream) {
@@ -882,6 +940,66 @@ nm_status nm_spmm_gather_ex(const nm_handle* h, const void* Xt, int64_t ldx, int
 }  // extern "C"
 
 namespace {
+
+nm_status compress_rows(const void* W_dev, int64_t n_out, int64_t k, nm_dtype dt, int N, int M, bool gated,
+                        void* stream, nm_handle** out) {
+  g_err.clear();
+  if (!out) return fail(NM_ERR_INVALID, "null output handle pointer");
+  *out = nullptr;
+  if (!W_dev) return fail(NM_ERR_INVALID, "null W");
+  if ((int)dt < 0 || (int)dt > 2) return fail(NM_ERR_INVALID, "unknown dtype %d", (int)dt);
+  if (n_out <= 0 || k <= 0) return fail(NM_ERR_INVALID, "n_out and k must be positive");
+  if (n_out > (1 << 24) || k > (1 << 24)) return fail(NM_ERR_UNSUPPORTED, "n_out and k are limited to 2^24");
+  // INT8 accumulates exactly in int32: |acc| <= k * 128 * 127 must stay below 2^31.
+  if (dt == NM_INT8 && k > (1 << 17))
+    return fail(NM_ERR_UNSUPPORTED, "INT8 k is limited to 2^17 (int32 accumulation must not overflow)");
+  if (M <= 0 || N <= 0 || N > M) return fail(NM_ERR_INVALID, "bad N:M %d:%d", N, M);
+  bool sp24 = false;
+  if (!nm::pattern_supported(N, M, &sp24)) return fail(NM_ERR_UNSUPPORTED, "N:M %d:%d is not supported", N, M);
+  if (k % M != 0) return fail(NM_ERR_INVALID, "k=%lld is not a multiple of M=%d", (long long)k, M);
+  const int es = nm::elem_bytes((int)dt);
+  if (!aligned(W_dev, (size_t)es)) return fail(NM_ERR_INVALID, "W is not element aligned");
+
+  nm_handle* h = new (std::nothrow) nm_handle();
+  if (!h) return fail(NM_ERR_OOM, "host allocation failed");
+  cudaGetDevice(&h->device);
+  h->n_out = n_out;
+  h->k = k;
+  h->N = N;
+  h->M = M;
+  h->dt = (int)dt;
+  h->img = sp24 ? nm::IMG_SP24 : nm::IMG_DENSE;
+  const int KB = nm::kblock_elems(h->dt);
+  h->n_kb = (int)((k + KB - 1) / KB);
+  h->gated = gated ? 1 : 0;
+  h->n_ct = (int)(((gated ? nm::gated_packed_rows(n_out / 2) : n_out) + nm::kRows - 1) / nm::kRows);
+  h->chunk = (size_t)nm::chunk_bytes(h->dt, h->img);
+  h->values_bytes = (size_t)n_out * (size_t)(k / M) * N * es;
+  h->idx_pitch = ((k / M) * N + 1) / 2;
+  h->idx_bytes = (size_t)n_out * (size_t)h->idx_pitch;
+  h->bpack_bytes = (size_t)h->n_ct * h->n_kb * h->chunk;
+
+  cudaError_t e;
+  nm_status st = NM_OK;
+  if ((e = cudaMalloc(&h->d_values, h->values_bytes)) != cudaSuccess) st = cuda_fail(e, "allocate values");
+  else if ((e = cudaMalloc(&h->d_idx, h->idx_bytes)) != cudaSuccess) st = cuda_fail(e, "allocate idx");
+  else if ((e = cudaMalloc(&h->d_bpack, h->bpack_bytes)) != cudaSuccess) st = cuda_fail(e, "allocate packed image");
+  else if ((e = cudaMalloc(&h->d_err, sizeof(int))) != cudaSuccess) st = cuda_fail(e, "allocate error word");
+  else if ((e = cudaMemsetAsync(h->d_err, 0, sizeof(int), (cudaStream_t)stream)) != cudaSuccess)
+    st = cuda_fail(e, "clear error word");
+  else if ((e = nm::launch_compress(h, W_dev, (cudaStream_t)stream)) != cudaSuccess)
+    st = cuda_fail(e, "launch compress kernel");
+  else
+    st = make_w_map(h);
+  if (st != NM_OK) {
+    const std::string msg = g_err;
+    nm_destroy(h);
+    g_err = msg;
+    return st;
+  }
+  *out = h;
+  return NM_OK;
+}
 
 nm_status gather_impl(const nm_handle* hc, const void* Xt, int64_t ldx, int64_t T, void* Y, const float* scale,
                       void* stream, const EpiReq* ep) {

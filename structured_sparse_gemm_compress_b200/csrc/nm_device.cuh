@@ -78,6 +78,11 @@ __host__ __device__ inline int64_t gated_source_row(int64_t r, int64_t n_ff) {
   const int64_t ch = (r >> 5) * 16 + (r & 15);
   return ch >= n_ff ? -1 : ((r & 16) ? n_ff + ch : ch);
 }
+// The packed row that holds row r of W.
+__host__ __device__ inline int64_t gated_packed_row(int64_t r, int64_t n_ff) {
+  const int64_t up = r >= n_ff ? 1 : 0, ch = r - up * n_ff;
+  return (ch >> 4) * 32 + up * 16 + (ch & 15);
+}
 __host__ __device__ inline int64_t gated_packed_rows(int64_t n_ff) { return (n_ff + 15) / 16 * 32; }
 
 // Offset of the scale byte of (row r, 32-block b) in microscaled scale tiles

@@ -132,6 +132,10 @@ struct SpmmArgs {
   // Before waiting for the previous kernel of the stream, hint into L2 the
   // first unit's weight chunks (1) and also its activation boxes (2); 0: none.
   int prefetch = 0;
+  // Gated output stage: rows of each half of W, and where p = acc * scale + bias
+  // goes ([T][2 n_ff] in the handle's type), or null.
+  int n_ff = 0;
+  void* P = nullptr;
 };
 
 // Timeline trace layout (builds with NM_TRACE): per CTA kTraceStride int64
@@ -158,5 +162,9 @@ int stream_max_clusters(int size);
 constexpr int kMaxClusterSplit = 8;
 cudaError_t launch_spmm(const nm_handle* h, const CUtensorMap* tmX, const CUtensorMap* tmY, const Plan& p,
                         const SpmmArgs& a, cudaStream_t s);
+
+// The gated output stage (handles of nm_compress_gated): a.out_ty, a.n_ff and a.P set.
+cudaError_t launch_spmm_gated(const nm_handle* h, const CUtensorMap& tmX, const Plan& p, const SpmmArgs& a,
+                              cudaStream_t s);
 
 }  // namespace nm

@@ -155,9 +155,10 @@ __device__ __forceinline__ void kept_selector(uint32_t m, uint32_t& sel, uint32_
 }
 
 template <int N, int M, int IMG>
-__device__ __forceinline__ void compress_unit_i8(const uint32_t (&w)[4], int64_t r, int64_t k0, int64_t K,
-                                                 int n_kb, int8_t* __restrict__ values, uint8_t* __restrict__ idx,
-                                                 int64_t idx_pitch, uint8_t* __restrict__ bpack) {
+__device__ __forceinline__ void compress_unit_i8(const uint32_t (&w)[4], int64_t r, int64_t src_row, int64_t k0,
+                                                 int64_t K, int n_kb, int8_t* __restrict__ values,
+                                                 uint8_t* __restrict__ idx, int64_t idx_pitch,
+                                                 uint8_t* __restrict__ bpack) {
   constexpr int G = 16 / M;
   constexpr int CNT = 16 * N / M;
   const uint32_t keep = keep_mask_i8<N, M>(w);
@@ -192,8 +193,8 @@ __device__ __forceinline__ void compress_unit_i8(const uint32_t (&w)[4], int64_t
   }
   const int64_t kept_per_row = (K / M) * N;
   const int64_t e0 = (k0 / M) * N;
-  uint8_t* vdst = reinterpret_cast<uint8_t*>(values + r * kept_per_row + e0);
-  uint8_t* idst = idx + r * idx_pitch + e0 / 2;
+  uint8_t* vdst = reinterpret_cast<uint8_t*>(values + src_row * kept_per_row + e0);
+  uint8_t* idst = idx + src_row * idx_pitch + e0 / 2;
   if constexpr (CNT >= 4) {
     store_bytes(vdst, vw, CNT);
   } else {
@@ -249,9 +250,11 @@ __device__ __forceinline__ void compress_unit_i8(const uint32_t (&w)[4], int64_t
   }
 }
 
+// n_ff > 0: a gated weight, whose packed row r holds row gated_source_row(r,
+// n_ff) of W; the canonical format keeps W's own row order.
 template <int DT, int N, int M>
 __global__ void __launch_bounds__(256) compress_kernel(const typename Elem<DT>::T* __restrict__ W, int64_t n_out,
-                                                       int64_t K, int n_kb, typename Elem<DT>::T* __restrict__ values,
+                                                       int64_t n_ff, int64_t K, int n_kb, typename Elem<DT>::T* __restrict__ values,
                                                        uint8_t* __restrict__ idx, int64_t idx_pitch,
                                                        uint8_t* __restrict__ bpack, int64_t total_units) {
   using T = typename Elem<DT>::T;
@@ -269,13 +272,15 @@ __global__ void __launch_bounds__(256) compress_kernel(const typename Elem<DT>::
   // ---- load 16 positions (zero beyond the row or beyond K)
   T raw[16];
   const int64_t rem = K - k0;
-  const int valid = r < n_out ? (int)(rem < 0 ? 0 : (rem > 16 ? 16 : rem)) : 0;
-  const T* src = W + r * K + k0;
+  const int64_t src_row = n_ff ? gated_source_row(r, n_ff) : (r < n_out ? r : -1);  // -1: padding
+  const int valid = src_row >= 0 ? (int)(rem < 0 ? 0 : (rem > 16 ? 16 : rem)) : 0;
+  const T* src = W + src_row * K + k0;
   if constexpr (DT == DT_I8) {
     if (valid == 16 && (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
       const uint4 q = __ldg(reinterpret_cast<const uint4*>(src));
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-      compress_unit_i8<N, M, IMG>(w, r, k0, K, n_kb, reinterpret_cast<int8_t*>(values), idx, idx_pitch, bpack);
+      compress_unit_i8<N, M, IMG>(w, r, src_row, k0, K, n_kb, reinterpret_cast<int8_t*>(values), idx, idx_pitch,
+                                  bpack);
       return;
     }
   }
@@ -310,8 +315,8 @@ __global__ void __launch_bounds__(256) compress_kernel(const typename Elem<DT>::
         nib[e / 8] |= (uint32_t)(p & 0xF) << (4 * (e % 8));
       }
     }
-    uint8_t* vdst = reinterpret_cast<uint8_t*>(values + r * kept_per_row + e0);
-    uint8_t* idst = idx + r * idx_pitch + e0 / 2;
+    uint8_t* vdst = reinterpret_cast<uint8_t*>(values + src_row * kept_per_row + e0);
+    uint8_t* idst = idx + src_row * idx_pitch + e0 / 2;
     if (valid == 16) {
       uint32_t vw[CNT * ES / 4 > 0 ? CNT * ES / 4 : 1];
       if constexpr (CNT * ES >= 4) {
@@ -334,7 +339,7 @@ __global__ void __launch_bounds__(256) compress_kernel(const typename Elem<DT>::
       }
     } else {  // ragged end of a row: only the groups that exist
       const int cnt = (valid / M) * N;
-      T* vd = values + r * kept_per_row + e0;
+      T* vd = values + src_row * kept_per_row + e0;
 #pragma unroll
       for (int e = 0; e < CNT; ++e)
         if (e < cnt) vd[e] = vals[e];
@@ -412,7 +417,7 @@ __global__ void __launch_bounds__(256) compress_kernel(const typename Elem<DT>::
 }
 
 template <int DT>
-__global__ void __launch_bounds__(256) decompress_kernel(const uint8_t* __restrict__ bpack, int64_t n_out,
+__global__ void __launch_bounds__(256) decompress_kernel(const uint8_t* __restrict__ bpack, int64_t n_ff,
                                                          int64_t K, int img, int n_kb,
                                                          typename Elem<DT>::T* __restrict__ Wout,
                                                          int64_t total_units) {
@@ -425,8 +430,9 @@ __global__ void __launch_bounds__(256) decompress_kernel(const uint8_t* __restri
   const int64_t r = unit / units_per_row;
   const int64_t k0 = (unit - r * units_per_row) * 16;
   const int valid = (int)(K - k0 > 16 ? 16 : K - k0);
-  const int64_t ct = r / kRows;
-  const uint32_t rr = (uint32_t)(r % kRows);
+  const int64_t pr = n_ff ? gated_packed_row(r, n_ff) : r;
+  const int64_t ct = pr / kRows;
+  const uint32_t rr = (uint32_t)(pr % kRows);
   const int kb = (int)(k0 / KB);
   const uint32_t kk = (uint32_t)(k0 % KB);
   const uint8_t* chunk = bpack + ((size_t)ct * n_kb + kb) * (size_t)chunk_bytes(DT, img);
@@ -636,7 +642,7 @@ static void launch_compress_t(const nm_handle* h, const void* W, int64_t total, 
   using T = typename Elem<DT>::T;
   const int threads = 256;
   const unsigned blocks = (unsigned)((total + threads - 1) / threads);
-  compress_kernel<DT, N, M><<<blocks, threads, 0, s>>>((const T*)W, h->n_out, h->k, h->n_kb, (T*)h->d_values,
+  compress_kernel<DT, N, M><<<blocks, threads, 0, s>>>((const T*)W, h->n_out, h->gated ? h->n_out / 2 : 0, h->k, h->n_kb, (T*)h->d_values,
                                                        h->d_idx, h->idx_pitch, h->d_bpack, total);
 }
 
@@ -731,15 +737,15 @@ cudaError_t launch_decompress(const nm_handle* h, void* Wout, cudaStream_t s) {
   const unsigned blocks = (unsigned)((total + threads - 1) / threads);
   switch (h->dt) {
     case DT_I8:
-      decompress_kernel<DT_I8><<<blocks, threads, 0, s>>>(h->d_bpack, h->n_out, h->k, h->img, h->n_kb,
+      decompress_kernel<DT_I8><<<blocks, threads, 0, s>>>(h->d_bpack, h->gated ? h->n_out / 2 : 0, h->k, h->img, h->n_kb,
                                                          (int8_t*)Wout, total);
       break;
     case DT_F16:
-      decompress_kernel<DT_F16><<<blocks, threads, 0, s>>>(h->d_bpack, h->n_out, h->k, h->img, h->n_kb,
+      decompress_kernel<DT_F16><<<blocks, threads, 0, s>>>(h->d_bpack, h->gated ? h->n_out / 2 : 0, h->k, h->img, h->n_kb,
                                                           (uint16_t*)Wout, total);
       break;
     default:
-      decompress_kernel<DT_BF16><<<blocks, threads, 0, s>>>(h->d_bpack, h->n_out, h->k, h->img, h->n_kb,
+      decompress_kernel<DT_BF16><<<blocks, threads, 0, s>>>(h->d_bpack, h->gated ? h->n_out / 2 : 0, h->k, h->img, h->n_kb,
                                                            (uint16_t*)Wout, total);
       break;
   }

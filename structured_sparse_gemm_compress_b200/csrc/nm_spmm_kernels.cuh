@@ -53,6 +53,10 @@ constexpr int kSmemBudget = 227 * 1024 - 1024;  // dynamic shared memory after 1
 // SpmmArgs; always with direct stores).
 constexpr int kOutDirect = 4;
 constexpr int kOutEpi = 8;
+// bit 4 = gated output stage (with bit 3): the handle's packed rows are 16 gate
+// channels beside their 16 up channels, so one warp's 32 lanes hold both halves
+// of 16 output channels.
+constexpr int kOutGate = 16;
 constexpr int out_bytes(int out) { return ((out & 3) == OUT_I32 || (out & 3) == OUT_F32) ? 4 : 2; }
 // Epilogue warps and CTA size of a kernel with output code OUT.
 constexpr int epi_warps(int out) { return 4 * epw_for((out & kOutEpi) != 0); }
@@ -366,6 +370,90 @@ __device__ __forceinline__ void epi_run(const SpmmArgs& a, const EpiCh& e, const
   }
 }
 
+// ---- gated output stage (OUT has kOutGate)
+//
+// p = acc * scale + bias per packed row as above, y = act(gate) * up.  A warp
+// holds 32 packed rows: lanes 0-15 the gate rows of 16 channels, lanes 16-31
+// their up rows, all for the same run of tokens.  Lane l and lane l ^ 16
+// exchange half a run each (one shuffle per two accumulators), after which the
+// lower lane has both halves for the run's first tokens and the upper lane for
+// the rest: every lane computes and stores as many outputs as any other.
+// What it costs against the ungated stage: half the stores, CH / 2 shuffles.
+template <int DT>
+__device__ __forceinline__ void gate_save(void* P, size_t i, float f) {  // p in the handle's type
+  if constexpr (DT == DT_F16)
+    reinterpret_cast<__half*>(P)[i] = __float2half_rn(f);
+  else if constexpr (DT == DT_BF16)
+    reinterpret_cast<__nv_bfloat16*>(P)[i] = __float2bfloat16_rn(f);
+}
+
+// p of one accumulator.
+template <int DT>
+__device__ __forceinline__ float gate_value(uint32_t acc, const EpiCh& e, const SpmmArgs& a) {
+  float f = DT == DT_I8 ? __int2float_rn((int32_t)acc) : __uint_as_float(acc);
+  if (a.scale) f = __fmul_rn(f, e.s);
+  if (a.bias) f = __fadd_rn(f, e.b);
+  return f;
+}
+
+template <int OT, int H>
+__device__ __forceinline__ void gate_store(const SpmmArgs& a, const float (&y)[H], size_t base, int nvalid) {
+#pragma unroll
+  for (int j = 0; j < H; ++j)
+    if (j < nvalid) epi_put<OT>(a.Y, base + (size_t)j * a.n_ff, y[j], a.out_scale);
+}
+
+// One warp's run of CH tokens starting at token t0; row: this lane's packed row.
+template <int DT, int CH>
+__device__ __forceinline__ void gate_run(const SpmmArgs& a, const EpiCh& e, const uint32_t (&r)[CH], int row, int t0,
+                                         int lane) {
+  constexpr int H = CH / 2;
+  float f[CH];
+#pragma unroll
+  for (int j = 0; j < CH; ++j) f[j] = DT == DT_I8 ? __int2float_rn((int32_t)r[j]) : __uint_as_float(r[j]);
+  if (a.scale) {
+    const uint64_t s2 = pk2(e.s, e.s);
+#pragma unroll
+    for (int j = 0; j < CH; j += 2) upk2(mul2(pk2(f[j], f[j + 1]), s2), f[j], f[j + 1]);
+  }
+  if (a.bias) {
+    const uint64_t b2 = pk2(e.b, e.b);
+#pragma unroll
+    for (int j = 0; j < CH; j += 2) upk2(add2(pk2(f[j], f[j + 1]), b2), f[j], f[j + 1]);
+  }
+  const int ch = (row >> 5) * 16 + (row & 15);
+  const bool ch_ok = ch < a.n_ff;
+  if constexpr (DT != DT_I8) {
+    if (a.P && ch_ok) {
+      const size_t base = (size_t)t0 * (2 * (size_t)a.n_ff) + (size_t)((row & 16) ? a.n_ff + ch : ch);
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+        if (t0 + j < a.T) gate_save<DT>(a.P, base + (size_t)j * (2 * (size_t)a.n_ff), f[j]);
+    }
+  }
+  __syncwarp();
+  const bool up = (lane & 16) != 0;
+  float g[H], u[H];
+#pragma unroll
+  for (int j = 0; j < H; ++j) {
+    const float got = __shfl_xor_sync(0xffffffffu, up ? f[j] : f[j + H], 16);
+    g[j] = up ? got : f[j];
+    u[j] = up ? f[j + H] : got;
+  }
+  act_run<H>(g, a.act);
+#pragma unroll
+  for (int j = 0; j < H; ++j) g[j] = __fmul_rn(g[j], u[j]);
+  if (!ch_ok) return;
+  const int ty = up ? t0 + H : t0;
+  const size_t base = (size_t)ty * a.n_ff + ch;
+  switch (a.out_ty) {
+    case OUT_F16: gate_store<OUT_F16, H>(a, g, base, a.T - ty); break;
+    case OUT_BF16: gate_store<OUT_BF16, H>(a, g, base, a.T - ty); break;
+    case OUT_I8: gate_store<OUT_I8, H>(a, g, base, a.T - ty); break;
+    default: gate_store<OUT_F32, H>(a, g, base, a.T - ty); break;
+  }
+}
+
 // A single element (split-K reduction).
 template <int DT>
 __device__ __forceinline__ void epi_one(const SpmmArgs& a, const EpiCh& e, size_t i, uint32_t acc) {
@@ -488,6 +576,72 @@ __device__ __forceinline__ void csplit_reduce(const SpmmArgs& a, const Unit& w, 
   }
 }
 
+// The gated form: half a warp finishes a token, each lane four gate rows and the
+// four up rows beside them.
+template <int DT, int BN, int EPI_WARPS>
+__device__ __forceinline__ void csplit_reduce_gated(const SpmmArgs& a, const Unit& w, uint32_t xb_local, int ew,
+                                                    int lane) {
+  const int S = a.splits;
+  uint32_t src[kMaxClusterSplit];
+#pragma unroll
+  for (int z = 0; z < kMaxClusterSplit; ++z) src[z] = z < S ? mapa_shared(xb_local, (uint32_t)z) : 0u;
+  const int l = lane & 15;
+  const int rl = (l >> 2) * 32 + (l & 3) * 4;                // first gate row within the tile
+  const int ch = w.ct * (kRows / 2) + (l >> 2) * 16 + (l & 3) * 4;
+  if (ch >= a.n_ff) return;
+  EpiCh eg[4], eu[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool ok = ch + i < a.n_ff;
+    eg[i].s = (a.scale && ok) ? __ldg(a.scale + ch + i) : 1.0f;
+    eu[i].s = (a.scale && ok) ? __ldg(a.scale + a.n_ff + ch + i) : 1.0f;
+    eg[i].b = (a.bias && ok) ? __ldg(a.bias + ch + i) : 0.0f;
+    eu[i].b = (a.bias && ok) ? __ldg(a.bias + a.n_ff + ch + i) : 0.0f;
+  }
+#pragma unroll 1
+  for (int j = w.z + S * (2 * ew + (lane >> 4)); j < BN; j += 2 * S * EPI_WARPS) {
+    const int t = w.tt * BN + j;
+    if (t >= a.T) break;  // columns ascend: the rest are beyond T too
+    const uint32_t off = (uint32_t)(j * kRows + rl) * 4u;
+    uint32_t g[4] = {0u, 0u, 0u, 0u}, u[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int z = 0; z < kMaxClusterSplit; ++z) {
+      if (z < S) {
+        const uint4 vg = ld_cluster_v4(src[z] + off), vu = ld_cluster_v4(src[z] + off + 64u);
+        g[0] = z ? add_acc<DT>(g[0], vg.x) : vg.x;
+        g[1] = z ? add_acc<DT>(g[1], vg.y) : vg.y;
+        g[2] = z ? add_acc<DT>(g[2], vg.z) : vg.z;
+        g[3] = z ? add_acc<DT>(g[3], vg.w) : vg.w;
+        u[0] = z ? add_acc<DT>(u[0], vu.x) : vu.x;
+        u[1] = z ? add_acc<DT>(u[1], vu.y) : vu.y;
+        u[2] = z ? add_acc<DT>(u[2], vu.z) : vu.z;
+        u[3] = z ? add_acc<DT>(u[3], vu.w) : vu.w;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (ch + i >= a.n_ff) break;
+      const float pg = gate_value<DT>(g[i], eg[i], a), pu = gate_value<DT>(u[i], eu[i], a);
+      if constexpr (DT != DT_I8) {
+        if (a.P) {
+          gate_save<DT>(a.P, (size_t)t * (2 * (size_t)a.n_ff) + ch + i, pg);
+          gate_save<DT>(a.P, (size_t)t * (2 * (size_t)a.n_ff) + a.n_ff + ch + i, pu);
+        }
+      }
+      float y[2] = {pg, 0.0f};
+      act_run<2>(y, a.act);
+      const float v = __fmul_rn(y[0], pu);
+      const size_t o = (size_t)t * a.n_ff + ch + i;
+      switch (a.out_ty) {
+        case OUT_F16: epi_put<OUT_F16>(a.Y, o, v, a.out_scale); break;
+        case OUT_BF16: epi_put<OUT_BF16>(a.Y, o, v, a.out_scale); break;
+        case OUT_I8: epi_put<OUT_I8>(a.Y, o, v, a.out_scale); break;
+        default: epi_put<OUT_F32>(a.Y, o, v, a.out_scale); break;
+      }
+    }
+  }
+}
+
 template <int DT, int IMG, int BN, int OUT, int XKB>
 __global__ void __launch_bounds__(kernel_threads(IMG, OUT), 1)
     spmm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY,
@@ -496,7 +650,9 @@ __global__ void __launch_bounds__(kernel_threads(IMG, OUT), 1)
   constexpr bool XS = C::XS;
   constexpr bool SP = C::SP;
   constexpr bool EPI = (OUT & kOutEpi) != 0;
+  constexpr bool GATE = (OUT & kOutGate) != 0;
   static_assert(!EPI || !C::TS, "the runtime output stage stores directly");
+  static_assert(!GATE || EPI, "the gated output stage is a runtime one");
   constexpr int KIND = DT == DT_I8 ? 0 : 1;
 
   extern __shared__ uint8_t smem_raw[];
@@ -883,10 +1039,12 @@ __global__ void __launch_bounds__(kernel_threads(IMG, OUT), 1)
       tc_fence_after();
       const int ch0 = w.ct * kRows + lq * 32;  // first channel of this warp's lane quarter
       const int ch = ch0 + lane;
-      const bool ch_ok = ch < a.n_out;
+      // this lane's row of W (gated: interleaved packed rows)
+      const int wrow = GATE ? (int)gated_source_row(ch, a.n_ff) : ch;
+      const bool ch_ok = GATE ? wrow >= 0 : ch < a.n_out;
       const bool has_scale = a.scale != nullptr;
-      const float s = (has_scale && ch_ok) ? __ldg(a.scale + ch) : 1.0f;
-      const float bch = (EPI && a.bias && ch_ok) ? __ldg(a.bias + ch) : 0.0f;
+      const float s = (has_scale && ch_ok) ? __ldg(a.scale + wrow) : 1.0f;
+      const float bch = (EPI && a.bias && ch_ok) ? __ldg(a.bias + wrow) : 0.0f;
       const int col0 = part * C::WCOLS;        // first token column of this warp within the tile
       const int t0 = w.tt * BN + col0;
       const uint32_t tbase = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * BN + col0);
@@ -920,6 +1078,8 @@ __global__ void __launch_bounds__(kernel_threads(IMG, OUT), 1)
               bulk_commit();
             }
             if (C::EPI_NB == 2) buf ^= 1;
+          } else if constexpr (GATE) {
+            gate_run<DT, C::CH>(a, EpiCh{s, bch}, r, ch, tc0, lane);
           } else if (ch_ok) {
             if constexpr (EPI) {
               epi_run<DT, C::CH>(a, EpiCh{s, bch}, r, (size_t)tc0 * a.n_out + ch, a.T - tc0);
@@ -955,7 +1115,7 @@ __global__ void __launch_bounds__(kernel_threads(IMG, OUT), 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&acce_bar[acc]);
         }
-      } else {
+      } else if constexpr (!GATE) {  // gated products split on chip only
         // split-K: publish this split's partial tile, the last arriving split reduces
         uint32_t* part = reinterpret_cast<uint32_t*>(a.ws);
         const size_t tile_elems = (size_t)BN * kRows;
@@ -1028,8 +1188,12 @@ __global__ void __launch_bounds__(kernel_threads(IMG, OUT), 1)
       __syncwarp();
       cluster_arrive();
       cluster_wait();
-      if (warp >= 2 && warp < 2 + C::EPI_WARPS)
-        csplit_reduce<DT, BN, OUT, C::EPI_WARPS>(a, decode_unit(ur.first, a), smem_u32(smem), warp - 2, lane);
+      if (warp >= 2 && warp < 2 + C::EPI_WARPS) {
+        if constexpr (GATE)
+          csplit_reduce_gated<DT, BN, C::EPI_WARPS>(a, decode_unit(ur.first, a), smem_u32(smem), warp - 2, lane);
+        else
+          csplit_reduce<DT, BN, OUT, C::EPI_WARPS>(a, decode_unit(ur.first, a), smem_u32(smem), warp - 2, lane);
+      }
       __syncwarp();
       cluster_arrive();
       cluster_wait();
@@ -1107,7 +1271,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(cta_threads(OUT), 1)
   using C = PairCfg<DT, IMG, BN, OUT>;
   constexpr bool SP = C::SP;
   constexpr bool EPI = (OUT & kOutEpi) != 0;
+  constexpr bool GATE = (OUT & kOutGate) != 0;
   static_assert(!EPI || !C::TS, "the runtime output stage stores directly");
+  static_assert(!GATE || EPI, "the gated output stage is a runtime one");
   constexpr int KIND = DT == DT_I8 ? 0 : 1;
 
   extern __shared__ uint8_t smem_raw[];
@@ -1344,10 +1510,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(cta_threads(OUT), 1)
       tc_fence_after();
       const int ch0 = ct * kRows + lq * 32;
       const int ch = ch0 + lane;
-      const bool ch_ok = ch < a.n_out;
+      // this lane's row of W (gated: interleaved packed rows)
+      const int wrow = GATE ? (int)gated_source_row(ch, a.n_ff) : ch;
+      const bool ch_ok = GATE ? wrow >= 0 : ch < a.n_out;
       const bool has_scale = a.scale != nullptr;
-      const float s = (has_scale && ch_ok) ? __ldg(a.scale + ch) : 1.0f;
-      const float bch = (EPI && a.bias && ch_ok) ? __ldg(a.bias + ch) : 0.0f;
+      const float s = (has_scale && ch_ok) ? __ldg(a.scale + wrow) : 1.0f;
+      const float bch = (EPI && a.bias && ch_ok) ? __ldg(a.bias + wrow) : 0.0f;
       const int col0 = part * C::WCOLS;
       const int t0 = tt * BN + col0;
       const uint32_t tbase = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * BN + col0);
@@ -1385,6 +1553,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(cta_threads(OUT), 1)
             bulk_commit();
           }
           if (C::EPI_NB == 2) buf ^= 1;
+        } else if constexpr (GATE) {
+          gate_run<DT, C::CH>(a, EpiCh{s, bch}, r, ch, tc0, lane);
         } else if (ch_ok) {
           if constexpr (EPI) {
             epi_run<DT, C::CH>(a, EpiCh{s, bch}, r, (size_t)tc0 * a.n_out + ch, a.T - tc0);
