@@ -105,9 +105,16 @@ def _check(status: int) -> None:
         raise NMError(status, lib().nm_last_error().decode(errors="replace"))
 
 
+# The current device and its current stream's raw handle, without building a
+# torch.cuda.Stream object per call (3 us of an 8 us call).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -120,8 +127,8 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
     """An output that belongs to the stream the call runs on (torch's allocator
     then never hands its memory to work that is not ordered behind it)."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+    if stream is None:  # (empty_strided: two thirds of torch.empty's time per call)
+        return torch.empty_strided(shape, (1,) if len(shape) == 1 else (shape[1], 1), dtype=dtype, device=device)
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(s):
         return torch.empty(shape, dtype=dtype, device=device)
@@ -129,9 +136,9 @@ def _empty(shape, dtype, device, stream) -> torch.Tensor:
 
 def _check_tensor(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> None:
     """A contiguous tensor of this type and shape on the current CUDA device."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != _current_device():
         raise ValueError(f"{name} must be on the current CUDA device")
 
 
@@ -418,7 +425,7 @@ def nm_mx_quantize(X: torch.Tensor, Q: torch.Tensor | None = None, S: torch.Tens
     multiple of 16 bytes) to microscaled 4-bit codes Q [T, k / 2] and scales S (uint8)."""
     if X.dim() != 2 or X.dtype not in _MX_DT or (X.shape[1] > 1 and X.stride(1) != 1):
         raise ValueError("X must be a [T, k] float32/float16/bfloat16 tensor with contiguous rows")
-    if not X.is_cuda or X.get_device() != torch.cuda.current_device():
+    if not X.is_cuda or X.get_device() != _current_device():
         raise ValueError("X must be on the current CUDA device")
     T, k = X.shape
     n = (T + 127) // 128 * ((k + 255) // 256) * 1024

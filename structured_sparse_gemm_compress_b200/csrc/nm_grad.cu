@@ -84,18 +84,19 @@ __device__ __forceinline__ void dp_store(uint16_t* row, int f0, int F, int lane,
 // tensor core; columns n_ff .. pitch are never read) and, with `part`, the fp32
 // column sums of this block's rows ([row block][2][n_ff]), each warp's rows in
 // ascending order, the warps in order.  Memory bound.
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(32 * kDpWarps)
+// BIAS is its own instance: the sums' registers cost the plain one a third of its
+// warps.
+template <int DT, bool VEC, bool BIAS>
+__global__ void __launch_bounds__(32 * kDpWarps, BIAS ? 3 : 4)
     gated_dp_kernel(const uint16_t* __restrict__ P, const uint16_t* __restrict__ dY, int T, int F, int pitch, int act,
                     uint16_t* __restrict__ dp, float* __restrict__ part) {
-  __shared__ float sums[kDpWarps][2][kDpCols];
+  __shared__ float sums[BIAS ? kDpWarps : 1][2][kDpCols];
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int f0 = blockIdx.x * kDpCols, t0 = blockIdx.y * kDpRows;
   const int t1 = min(T, t0 + kDpRows);
   float sg[8] = {}, su[8] = {};
-#pragma unroll 2
   for (int t = t0 + warp; t < t1; t += kDpWarps) {
     const uint16_t* prow = P + (size_t)t * 2 * F;
     float g[8], u[8], dy[8];
@@ -108,26 +109,29 @@ __global__ void __launch_bounds__(32 * kDpWarps)
       act_slope(g[j], act, a, d);
       g[j] = __fmul_rn(__fmul_rn(dy[j], u[j]), d);
       u[j] = __fmul_rn(dy[j], a);
-      sg[j] += g[j];
-      su[j] += u[j];
+      if constexpr (BIAS) {
+        sg[j] += g[j];
+        su[j] += u[j];
+      }
     }
     uint16_t* out = dp + (size_t)t * 2 * pitch;
     dp_store<DT, VEC>(out, f0, F, lane, g);
     dp_store<DT, VEC>(out + pitch, f0, F, lane, u);
   }
-  if (!part) return;
+  if constexpr (BIAS) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    sums[warp][0][dp_col<VEC>(lane, j)] = sg[j];
-    sums[warp][1][dp_col<VEC>(lane, j)] = su[j];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * kDpCols; i += 32 * kDpWarps) {
-    const int z = i / kDpCols, c = i % kDpCols;
-    float s = 0.0f;
+    for (int j = 0; j < 8; ++j) {
+      sums[warp][0][dp_col<VEC>(lane, j)] = sg[j];
+      sums[warp][1][dp_col<VEC>(lane, j)] = su[j];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * kDpCols; i += 32 * kDpWarps) {
+      const int z = i / kDpCols, c = i % kDpCols;
+      float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kDpWarps; ++w) s += sums[w][z][c];
-    if (f0 + c < F) part[((size_t)blockIdx.y * 2 + z) * F + f0 + c] = s;
+      for (int w = 0; w < kDpWarps; ++w) s += sums[w][z][c];
+      if (f0 + c < F) part[((size_t)blockIdx.y * 2 + z) * F + f0 + c] = s;
+    }
   }
 }
 
@@ -158,8 +162,8 @@ __global__ void __launch_bounds__(256) dbias_kernel(const float* __restrict__ pa
 //   dW tile: rows f of one half, columns k; A = dp^T (MN-major), B = X (MN-major)
 //   dX tile: rows t,             columns k; A = dp (K-major),     B = Wm (MN-major)
 // A stage holds 64 summed elements: 16 KB of A and BN / 2 columns of B per CTA.
-// Two accumulators of BN columns; 16-bit output through staged tensor stores.
-// Every copy is zero-filled outside its tensor, so ragged sizes need no masks.
+// Two accumulators of BN columns; 16-bit output through staged rows.  Every copy
+// is zero-filled outside its tensor, so ragged sizes need no masks.
 constexpr int kGradKb = 64;
 constexpr int kGradEpiWarps = 8;
 constexpr int kGradThreads = 64 + 32 * kGradEpiWarps;
@@ -170,7 +174,7 @@ struct GradCfg {
   static constexpr int RUN = kGradKb * 128;            // one 128-byte run of an MN-major operand: 64 rows
   static constexpr int NB = BN / 128;                  // runs of B per CTA
   static constexpr int STAGE = A_BYTES + NB * RUN;
-  static constexpr int EPI_BUF = 4096;                 // two staged tiles of 32 rows x 64 bytes
+  static constexpr int EPI_BUF = 4096;                 // 32 staged rows of 128 bytes
   static constexpr int EPI_BYTES = kGradEpiWarps * EPI_BUF;
   static constexpr int STAGES_FIT = (227 * 1024 - 1024 - EPI_BYTES) / STAGE;
   static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
@@ -194,6 +198,7 @@ struct GradArgs {
   int hi_tiles, lo_tiles;  // tiles of side 1 for those pairs, and for the others
   int F, T, k;
   int kb_half;       // dX: stages per half of 2 n_ff
+  void *dW, *dX;
   int* err;
   unsigned long long timeout_ns;
 };
@@ -250,7 +255,6 @@ template <int DT, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     grad_pair_kernel(const __grid_constant__ CUtensorMap tmPw, const __grid_constant__ CUtensorMap tmPx,
                      const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                     const __grid_constant__ CUtensorMap tmDW, const __grid_constant__ CUtensorMap tmDX,
                      const GradArgs a) {
   using C = GradCfg<BN>;
   extern __shared__ uint8_t smem_raw[];
@@ -259,6 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
   __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
   __shared__ __align__(8) uint64_t accf_bar[2];
   __shared__ __align__(8) uint64_t acce_bar[2];
+  __shared__ __align__(8) uint64_t pfree_bar[2];  // peer: its epilogue warps have read accumulator i
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_sh;
@@ -273,7 +278,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&accf_bar[i], 1);
-      mbar_init(&acce_bar[i], 2 * kGradEpiWarps);
+      mbar_init(&acce_bar[i], kGradEpiWarps + 1);  // the leader's epilogue warps, and one arrive for all the peer's
+      mbar_init(&pfree_bar[i], kGradEpiWarps);
     }
     mbar_init(&drain_bar, 1);
     abort_sh = 0;
@@ -390,14 +396,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         }
       }
       if (issuer) tc_commit_pair(&drain_bar, (uint16_t)3);
+    } else {
+      // Peer: turn each accumulator release of this CTA's epilogue warps into one
+      // cluster-scope arrive on the leader (theirs would first wait for their own
+      // output stores to become visible; this warp has none in flight).
+      const bool issuer = elect_one();
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      for (int i = 0; grad_unit(a, pair, pairs, i, BN, u); ++i) {
+        if (!mbar_wait_warp(&pfree_bar[acc], acc_phase, &abort_sh, tmo)) {
+          if (issuer) give_up(4);
+          break;
+        }
+        if (issuer) mbar_arrive_cluster(acce_lead0 + 8u * (uint32_t)acc);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
     }
     mbar_wait_warp(&drain_bar, 0, &abort_sh, tmo);  // every MMA of this pair has completed
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
     constexpr int OT = DT == DT_F16 ? OUT_F16 : OUT_BF16;
     const int ew = warp - 2, lq = warp & 3, part = ew >> 2;
-    uint8_t* stage_buf = smem + (size_t)C::STAGES * C::STAGE + (size_t)ew * C::EPI_BUF;
-    int acc = 0, buf = 0;
+    uint8_t* buf = smem + (size_t)C::STAGES * C::STAGE + (size_t)ew * C::EPI_BUF;
+    int acc = 0;
     uint32_t acc_phase = 0;
     for (int i = 0; grad_unit(a, pair, pairs, i, BN, u); ++i) {
       if (!mbar_wait_warp(&accf_bar[acc], acc_phase, &abort_sh, tmo)) {
@@ -406,44 +430,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
       }
       tc_fence_after();
       const int row0 = u.m0 + (int)rank * 128 + lq * 32, col0 = u.n0 + part * C::WCOLS;
-      const bool rows_in = row0 < (u.dw ? a.F : a.T);
-      const uint32_t tbase = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * BN + part * C::WCOLS);
+      const int rows = min(32, (u.dw ? a.F : a.T) - row0);
+      uint8_t* out = static_cast<uint8_t*>(u.dw ? a.dW : a.dX) +
+                     ((int64_t)(u.dw ? u.z * a.F : 0) + row0) * a.k * 2;
+      const uint32_t taddr = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * BN + part * C::WCOLS);
 #pragma unroll 1
-      for (int c = 0; c < C::WCOLS; c += 32) {
-        uint32_t r[32];
-        __syncwarp();
-        tmem_ld32(tbase + (uint32_t)c, r);
-        tmem_wait_ld();
-        if (c + 32 == C::WCOLS) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(acce_lead0 + 8u * (uint32_t)acc);
-        }
-        float v[32];
+      for (int c = 0; c < C::WCOLS; c += 64) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-        if (lane == 0) bulk_wait_read<1>();  // the staged tile that is about to be overwritten has been read
-        __syncwarp();
-        uint8_t* sb = stage_buf + buf * (C::EPI_BUF / 2);
-        stage_row<OT, 32>(sb, (uint32_t)lane, v);
-        fence_async_smem();
-        __syncwarp();
-        // columns at or beyond k are clipped by the store; a box wholly outside is not issued
-        if (lane == 0 && rows_in && col0 + c < a.k) {
-          if (u.dw)
-            tma_store_3d(&tmDW, sb, col0 + c, row0, u.z);
-          else
-            tma_store_3d(&tmDX, sb, col0 + c, row0, 0);
-          bulk_commit();
+        for (int h = 0; h < 2; ++h) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld32(taddr + (uint32_t)(c + 32 * h), r);
+          tmem_wait_ld();
+          if (h == 1 && c + 64 == C::WCOLS) {  // the peer's release is forwarded by its warp 1
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(leader ? &acce_bar[acc] : &pfree_bar[acc]);
+          }
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+          stage_row<OT, 128, 32>(buf, (uint32_t)lane, (uint32_t)(4 * h), v);
         }
-        buf ^= 1;
+        __syncwarp();
+        if (rows > 0 && col0 + c < a.k)
+          stage_flush<128>(buf, out + (int64_t)(col0 + c) * 2, (int64_t)a.k * 2, rows, min(64, a.k - col0 - c) * 2, true, 2,
+                           lane);
+        __syncwarp();
       }
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
       }
     }
-    if (lane == 0) bulk_wait<0>();  // this warp's tensor stores are complete before the CTA exits
   }
 
   tc_fence_before();
@@ -456,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
 }
 
 struct GradMaps {
-  CUtensorMap pw, px, x, w, dw, dx;
+  CUtensorMap pw, px, x, w;
 };
 
 template <int DT, int BN>
@@ -465,8 +484,7 @@ cudaError_t launch_grad_t(int grid, const GradMaps& m, const GradArgs& a, cudaSt
   static std::atomic<uint64_t> opted{0};
   cudaError_t e = smem_opt_in(kern, GradCfg<BN>::SMEM, opted);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3((unsigned)(2 * grid)), kGradThreads, GradCfg<BN>::SMEM, s, 0, m.pw, m.px, m.x, m.w, m.dw,
-                    m.dx, a);
+  return launch_pdl(kern, dim3((unsigned)(2 * grid)), kGradThreads, GradCfg<BN>::SMEM, s, 0, m.pw, m.px, m.x, m.w, a);
 }
 
 template <int DT>
@@ -475,8 +493,9 @@ cudaError_t launch_dp(bool vec, const void* P, const void* dY, int T, int F, int
   const dim3 grid((unsigned)((F + kDpCols - 1) / kDpCols), (unsigned)((T + kDpRows - 1) / kDpRows));
   const uint16_t *p = static_cast<const uint16_t*>(P), *y = static_cast<const uint16_t*>(dY);
   uint16_t* o = static_cast<uint16_t*>(dp);
-  return vec ? launch_pdl(gated_dp_kernel<DT, true>, grid, 32 * kDpWarps, 0, s, 0, p, y, T, F, pitch, act, o, part)
-             : launch_pdl(gated_dp_kernel<DT, false>, grid, 32 * kDpWarps, 0, s, 0, p, y, T, F, pitch, act, o, part);
+  auto kern = vec ? (part ? gated_dp_kernel<DT, true, true> : gated_dp_kernel<DT, true, false>)
+                  : (part ? gated_dp_kernel<DT, false, true> : gated_dp_kernel<DT, false, false>);
+  return launch_pdl(kern, grid, 32 * kDpWarps, 0, s, 0, p, y, T, F, pitch, act, o, part);
 }
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -585,6 +604,8 @@ nm_status nm_gated_backward(const nm_handle* h, const void* X, const void* P, co
     a.F = (int)F;
     a.T = (int)T;
     a.k = (int)h->k;
+    a.dW = dW;
+    a.dX = dX;
     a.err = h->d_err;
     a.timeout_ns = 1000000000ull;
     a.kb_half = (int)((F + kGradKb - 1) / kGradKb);
@@ -624,14 +645,11 @@ nm_status nm_gated_backward(const nm_handle* h, const void* X, const void* P, co
     const int dt = h->dt;
     const void* wm = base + lay.wm;
     const auto k128 = CU_TENSOR_MAP_SWIZZLE_128B;
-    const auto k64 = CU_TENSOR_MAP_SWIZZLE_64B;
     st = map16(&m.pw, dt, dp, F, 2, T, lay.pitch, 2 * lay.pitch, 64, 1, 64, k128);
     if (st == NM_OK) st = map16(&m.px, dt, dp, F, 2, T, lay.pitch, 2 * lay.pitch, 64, 1, 128, k128);
-    m.x = m.w = m.dw = m.dx = m.pw;  // of a product that is not asked for: never read
+    m.x = m.w = m.pw;  // of a product that is not asked for: never read
     if (st == NM_OK && dW) st = map16(&m.x, dt, X, h->k, T, 1, h->k, h->k * T, 64, 64, 1, k128);
-    if (st == NM_OK && dW) st = map16(&m.dw, dt, dW, h->k, F, 2, h->k, h->k * F, 32, 32, 1, k64);
     if (st == NM_OK && dX) st = map16(&m.w, dt, wm, h->k, F, 2, h->k, h->k * F, 64, 64, 1, k128);
-    if (st == NM_OK && dX) st = map16(&m.dx, dt, dX, h->k, T, 1, h->k, h->k * T, 32, 32, 1, k64);
     if (st != NM_OK) return st;
     e = dt == DT_F16 ? (bn == 256 ? launch_grad_t<DT_F16, 256>(grid, m, a, s) : launch_grad_t<DT_F16, 128>(grid, m, a, s))
                      : (bn == 256 ? launch_grad_t<DT_BF16, 256>(grid, m, a, s)

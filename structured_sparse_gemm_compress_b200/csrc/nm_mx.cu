@@ -1,7 +1,7 @@
 // nm_mx.cu -- microscaled 4-bit floating point (include/nmspmm.h gives the
 // format): quantisation of activations and weights, the values back, and the
 // product of two quantised matrices on the block-scaled tensor core.
-#include <cfloat>
+#include <cstdlib>
 #include <new>
 #include <string>
 
@@ -251,13 +251,11 @@ cudaError_t launch_dequantize(const uint8_t* Q, const uint8_t* S, int64_t rows, 
 // Tokens are the accumulator's lanes, so a thread holds consecutive channels of
 // one token: scale, bias and activation need no exchange between threads, the
 // two halves of a gated pair (16 gate channels beside their 16 up channels) meet
-// in one thread, and the output leaves by tensor stores of 32-token boxes.
+// in one thread, and rows leave through a staged tile as whole lines.
 //
 // What bounds it: at k = 1024 the output's bytes (4 stages of 512 cycles feed a
 // tile whose stores take longer); at long k the tensor pipe.
 constexpr int kMxKb = 256;
-constexpr int kMxEpiWarps = 8;
-constexpr int kMxThreads = 64 + 32 * kMxEpiWarps;
 constexpr int kMxSmemBudget = 227 * 1024 - 1024;
 
 template <int BN>
@@ -267,15 +265,19 @@ struct MxCfg {
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int B_BYTES = HB * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES + 1024 + ATOMS * 1024;
-  static constexpr int EPI_BUF = 4096;                         // per warp: one or two staged tiles
-  static constexpr int EPI_BYTES = kMxEpiWarps * EPI_BUF;
+  // epilogue warps per lane quarter: 64 (BN = 64: 32) accumulator columns each
+  static constexpr int EPW = BN == 192 ? 3 : 2;
+  static constexpr int EPI_WARPS = 4 * EPW;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int EPI_BUF = 4096;                         // per warp: 32 staged rows of up to 128 bytes
+  static constexpr int EPI_BYTES = EPI_WARPS * EPI_BUF;
   static constexpr int STAGES_FIT = (kMxSmemBudget - EPI_BYTES) / STAGE;
   static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
   static constexpr int SMEM = STAGES * STAGE + EPI_BYTES + 1024;
   static constexpr int SF_COLS = 8 + 8 * ATOMS;                // scale columns of one stage
   static constexpr int COLS_NEEDED = 2 * BN + 2 * SF_COLS;
   static constexpr int TMEM_COLS = COLS_NEEDED <= 256 ? 256 : 512;
-  static constexpr int WCOLS = BN / (kMxEpiWarps / 4);         // accumulator columns per epilogue warp
+  static constexpr int WCOLS = BN / EPW;                       // accumulator columns per epilogue warp
   static_assert(STAGE % 1024 == 0 && B_BYTES % 1024 == 0, "stages keep 1024-byte alignment");
   static_assert(STAGES >= 3 && COLS_NEEDED <= 512 && WCOLS % 32 == 0, "tile fits");
   // a tile starts at a multiple of BN: 64 rows into a scale tile at most
@@ -290,7 +292,8 @@ struct MxArgs {
   int T, n_y, n_acc, n_ff;   // tokens; output channels; accumulator channels; gated: n_ff, else 0
   int k, n_kb, n_tb, n_rb;   // k, 256-k blocks, 128-row scale tiles of X and of the weight
   int n_nt, units;
-  int out_ty, act, tma_store;
+  int out_ty, act;
+  int vec;                   // rows of Y start on 16 bytes
   unsigned long long timeout_ns;
 };
 
@@ -302,31 +305,80 @@ __host__ __device__ constexpr uint32_t mx_idesc(uint32_t sf_id) {
          (sf_id << 29);
 }
 
-template <int OT, int NV>
-__device__ __forceinline__ void mx_put(const MxArgs& a, const CUtensorMap* tmY, uint8_t* buf, const float* v, int row0,
-                                       int col0, int lane) {
-  stage_row<OT, NV>(buf, (uint32_t)lane, v);
-  if (a.tma_store) {
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0 && row0 < a.T && col0 < a.n_y) {
-      tma_store_2d(tmY, buf, col0, row0);
-      bulk_commit();
+// The output stage's share of one epilogue warp: WCOLS accumulator columns of its
+// 32 tokens, 32 at a time: scale, bias, activation (and gate), then staged rows
+// of up to 128 bytes.  `release` runs once the last columns are in registers.
+template <int OT, int WCOLS, bool GATED, typename Release>
+__device__ __forceinline__ void mx_epilogue(const MxArgs& a, uint32_t taddr, uint8_t* buf, float* vs, float* vb, int row0,
+                                            int col0, int lane, Release release) {
+  constexpr int ES = stage_elem_bytes(OT);
+  constexpr int NV = GATED ? 16 : 32;                         // outputs of one step
+  constexpr int OUTB = WCOLS / 32 * NV * ES;                  // output bytes of the warp's run of a row
+  constexpr int ROWB = OUTB >= 128 ? 128 : 64;                // (half of a 64-byte row stays unused at 32)
+  constexpr int STEPS = ROWB / (NV * ES) < WCOLS / 32 ? ROWB / (NV * ES) : WCOLS / 32;  // steps per staged tile
+  const int rows = min(32, a.T - row0);
+#pragma unroll
+  for (int c = 0; c < WCOLS / 32; ++c) {
+    const int col = col0 + 32 * c;
+    if (a.scale || a.bias) {  // this lane fetches the values of one accumulator column
+      const int ch = col + lane;
+      int src = ch;
+      bool in = ch < a.n_acc;
+      if constexpr (GATED) {
+        const int f = (ch >> 5) * 16 + (ch & 15);
+        in = f < a.n_ff;
+        src = (ch & 16) ? a.n_ff + f : f;
+      }
+      __syncwarp();
+      if (a.scale) vs[lane] = in ? __ldg(a.scale + src) : 0.0f;
+      if (a.bias) vb[lane] = in ? __ldg(a.bias + src) : 0.0f;
     }
-  } else {
+    uint32_t r[32];
     __syncwarp();
-    if (row0 < a.T && col0 < a.n_y)
-      stage_copy_rows<OT, NV>(buf, static_cast<uint8_t*>(a.Y) + ((int64_t)row0 * a.n_y + col0) * stage_elem_bytes(OT),
-                              a.n_y, min(32, a.T - row0), min(NV, a.n_y - col0), lane);
-    __syncwarp();
+    tmem_ld32(taddr + 32u * c, r);
+    tmem_wait_ld();
+    if (c == WCOLS / 32 - 1) release();
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+    if (a.scale) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 s4 = *reinterpret_cast<const float4*>(vs + j);
+        upk2(mul2(pk2(v[j], v[j + 1]), pk2(s4.x, s4.y)), v[j], v[j + 1]);
+        upk2(mul2(pk2(v[j + 2], v[j + 3]), pk2(s4.z, s4.w)), v[j + 2], v[j + 3]);
+      }
+    }
+    if (a.bias) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 b4 = *reinterpret_cast<const float4*>(vb + j);
+        upk2(add2(pk2(v[j], v[j + 1]), pk2(b4.x, b4.y)), v[j], v[j + 1]);
+        upk2(add2(pk2(v[j + 2], v[j + 3]), pk2(b4.z, b4.w)), v[j + 2], v[j + 3]);
+      }
+    }
+    act_run<NV>(v, a.act);
+    if constexpr (GATED) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], v[j + 16]);
+    }
+    stage_row<OT, ROWB, NV>(buf, (uint32_t)lane, (uint32_t)((c % STEPS) * NV * ES / 16), v);
+    if (c % STEPS == STEPS - 1) {
+      const int ycol = (GATED ? col0 / 2 : col0) + (c - (STEPS - 1)) * NV;
+      __syncwarp();
+      if (rows > 0 && ycol < a.n_y)
+        stage_flush<ROWB>(buf, static_cast<uint8_t*>(a.Y) + ((int64_t)row0 * a.n_y + ycol) * ES, (int64_t)a.n_y * ES,
+                          rows, min(STEPS * NV, a.n_y - ycol) * ES, a.vec != 0, ES, lane);
+      __syncwarp();
+    }
   }
 }
 
 template <int BN, bool GATED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxCfg<BN>::THREADS, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
-                   const __grid_constant__ CUtensorMap tmY, const MxArgs a) {
+                   const MxArgs a) {
   using C = MxCfg<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -334,8 +386,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
   __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
   __shared__ __align__(8) uint64_t accf_bar[2];
   __shared__ __align__(8) uint64_t acce_bar[2];
+  __shared__ __align__(8) uint64_t pfree_bar[2];  // peer: its epilogue warps have read accumulator i
   __shared__ __align__(8) uint64_t drain_bar;
-  __shared__ __align__(16) float vec_sh[kMxEpiWarps][2][32];
+  __shared__ __align__(16) float vec_sh[C::EPI_WARPS][2][32];
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_sh;
 
@@ -349,7 +402,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&accf_bar[i], 1);
-      mbar_init(&acce_bar[i], 2 * kMxEpiWarps);
+      mbar_init(&acce_bar[i], C::EPI_WARPS + 1);  // the leader's epilogue warps, and one arrive for all the peer's
+      mbar_init(&pfree_bar[i], C::EPI_WARPS);
     }
     mbar_init(&drain_bar, 1);
     abort_sh = 0;
@@ -360,7 +414,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
     prefetch_tensormap(&tmB);
     prefetch_tensormap(&tmSA);
     prefetch_tensormap(&tmSB);
-    if (a.tma_store) prefetch_tensormap(&tmY);
   }
   if (warp == 1) {
     tmem_alloc_cg<2>(&tmem_base_sh, C::TMEM_COLS);
@@ -483,16 +536,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
         }
       }
       if (issuer) tc_commit_pair(&drain_bar, (uint16_t)3);
+    } else {
+      // Peer: turn each accumulator release of this CTA's epilogue warps into one
+      // cluster-scope arrive on the leader (theirs would first wait for their own
+      // output stores to become visible; this warp has none in flight).
+      const bool issuer = elect_one();
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      for (int u = u_first; u < a.units; u += u_step) {
+        if (!mbar_wait_warp(&pfree_bar[acc], acc_phase, &abort_sh, tmo)) {
+          if (issuer) give_up(4);
+          break;
+        }
+        if (issuer) mbar_arrive_cluster(acce_lead0 + 8u * (uint32_t)acc);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
     }
     mbar_wait_warp(&drain_bar, 0, &abort_sh, tmo);  // every MMA of this pair has completed
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int ew = warp - 2, lq = warp & 3, part = ew >> 2;
-    uint8_t* stage_buf = smem + (size_t)C::STAGES * C::STAGE + (size_t)ew * C::EPI_BUF;
+    uint8_t* buf = smem + (size_t)C::STAGES * C::STAGE + (size_t)ew * C::EPI_BUF;
     float* vs = vec_sh[ew][0];
     float* vb = vec_sh[ew][1];
-    const bool wide = !GATED && a.out_ty == OUT_F32;  // a staged tile fills the warp's buffer
-    int acc = 0, buf = 0;
+    int acc = 0;
     uint32_t acc_phase = 0;
     for (int u = u_first; u < a.units; u += u_step) {
       const int nt = u % a.n_nt, mt = u / a.n_nt;
@@ -503,80 +573,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMxThreads, 1)
       tc_fence_after();
       const int row0 = mt * 256 + (int)rank * 128 + lq * 32;
       const int col0 = nt * BN + part * C::WCOLS;
-      const uint32_t tbase = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * BN + part * C::WCOLS);
-#pragma unroll 1
-      for (int c = 0; c < C::WCOLS; c += 32) {
-        const int ch = col0 + c + lane;  // this lane fetches the output stage's values of one channel
-        if (a.scale || a.bias) {
-          int src = ch;
-          bool in = ch < a.n_acc;
-          if constexpr (GATED) {
-            const int f = (ch >> 5) * 16 + (ch & 15);
-            in = f < a.n_ff;
-            src = (ch & 16) ? a.n_ff + f : f;
-          }
-          __syncwarp();
-          if (a.scale) vs[lane] = in ? __ldg(a.scale + src) : 0.0f;
-          if (a.bias) vb[lane] = in ? __ldg(a.bias + src) : 0.0f;
-        }
-        uint32_t r[32];
+      const uint32_t taddr = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * BN + part * C::WCOLS);
+      auto release = [&]() {  // the peer's release is forwarded by its warp 1
+        tc_fence_before();
         __syncwarp();
-        tmem_ld32(tbase + (uint32_t)c, r);
-        tmem_wait_ld();
-        if (c + 32 == C::WCOLS) {  // all of this warp's columns are in registers: release the accumulator
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(acce_lead0 + 8u * (uint32_t)acc);
-        }
-        float v[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-        if (a.scale) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 s4 = *reinterpret_cast<const float4*>(vs + j);
-            v[j] = __fmul_rn(v[j], s4.x);
-            v[j + 1] = __fmul_rn(v[j + 1], s4.y);
-            v[j + 2] = __fmul_rn(v[j + 2], s4.z);
-            v[j + 3] = __fmul_rn(v[j + 3], s4.w);
-          }
-        }
-        if (a.bias) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 b4 = *reinterpret_cast<const float4*>(vb + j);
-            v[j] = __fadd_rn(v[j], b4.x);
-            v[j + 1] = __fadd_rn(v[j + 1], b4.y);
-            v[j + 2] = __fadd_rn(v[j + 2], b4.z);
-            v[j + 3] = __fadd_rn(v[j + 3], b4.w);
-          }
-        }
-        constexpr int NV = GATED ? 16 : 32;
-        act_run<NV>(v, a.act);
-        if constexpr (GATED) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], v[j + 16]);
-        }
-        // the staged tile that is about to be overwritten has been read by its store
-        if (lane == 0) {
-          if (wide) bulk_wait_read<0>(); else bulk_wait_read<1>();
-        }
-        __syncwarp();
-        uint8_t* sb = stage_buf + (wide ? 0 : buf * (C::EPI_BUF / 2));
-        const int ycol = GATED ? (col0 + c) / 2 : col0 + c;
-        switch (a.out_ty) {
-          case OUT_F16: mx_put<OUT_F16, NV>(a, &tmY, sb, v, row0, ycol, lane); break;
-          case OUT_BF16: mx_put<OUT_BF16, NV>(a, &tmY, sb, v, row0, ycol, lane); break;
-          default: mx_put<OUT_F32, NV>(a, &tmY, sb, v, row0, ycol, lane); break;
-        }
-        buf ^= 1;
+        if (lane == 0) mbar_arrive(leader ? &acce_bar[acc] : &pfree_bar[acc]);
+      };
+      switch (a.out_ty) {
+        case OUT_F16: mx_epilogue<OUT_F16, C::WCOLS, GATED>(a, taddr, buf, vs, vb, row0, col0, lane, release); break;
+        case OUT_BF16: mx_epilogue<OUT_BF16, C::WCOLS, GATED>(a, taddr, buf, vs, vb, row0, col0, lane, release); break;
+        default: mx_epilogue<OUT_F32, C::WCOLS, GATED>(a, taddr, buf, vs, vb, row0, col0, lane, release); break;
       }
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
       }
     }
-    if (lane == 0) bulk_wait<0>();  // this warp's tensor stores are complete before the CTA exits
   }
 
   tc_fence_before();
@@ -593,23 +605,23 @@ constexpr int kMxTiles[3] = {192, 128, 64};
 
 template <int BN, bool GATED>
 cudaError_t launch_mx_t(const nm_handle* h, int slot, int grid, const CUtensorMap& tmA, const CUtensorMap& tmSA,
-                        const CUtensorMap& tmY, const MxArgs& a, cudaStream_t s) {
+                        const MxArgs& a, cudaStream_t s) {
   using C = MxCfg<BN>;
   auto kern = mx_pair_kernel<BN, GATED>;
   static std::atomic<uint64_t> opted{0};
   cudaError_t e = smem_opt_in(kern, C::SMEM, opted);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3((unsigned)(2 * grid)), kMxThreads, C::SMEM, s, 0, tmA, h->tm_mxq[slot], tmSA, h->tm_mxs,
-                    tmY, a);
+  return launch_pdl(kern, dim3((unsigned)(2 * grid)), C::THREADS, C::SMEM, s, 0, tmA, h->tm_mxq[slot], tmSA, h->tm_mxs,
+                    a);
 }
 
 template <bool GATED>
 cudaError_t launch_mx(const nm_handle* h, int slot, int grid, const CUtensorMap& tmA, const CUtensorMap& tmSA,
-                      const CUtensorMap& tmY, const MxArgs& a, cudaStream_t s) {
+                      const MxArgs& a, cudaStream_t s) {
   switch (slot) {
-    case 0: return launch_mx_t<kMxTiles[0], GATED>(h, slot, grid, tmA, tmSA, tmY, a, s);
-    case 1: return launch_mx_t<kMxTiles[1], GATED>(h, slot, grid, tmA, tmSA, tmY, a, s);
-    default: return launch_mx_t<kMxTiles[2], GATED>(h, slot, grid, tmA, tmSA, tmY, a, s);
+    case 0: return launch_mx_t<kMxTiles[0], GATED>(h, slot, grid, tmA, tmSA, a, s);
+    case 1: return launch_mx_t<kMxTiles[1], GATED>(h, slot, grid, tmA, tmSA, a, s);
+    default: return launch_mx_t<kMxTiles[2], GATED>(h, slot, grid, tmA, tmSA, a, s);
   }
 }
 
@@ -698,9 +710,12 @@ nm_status mx_product(const nm_handle* h, const void* Q, const void* S, int64_t T
   // Channel tile: the least rounds x (tile + fixed part) over the resident pairs.
   const int pairs = num_sms(h->device) / 2;
   const int64_t n_mt = (T + 255) / 256;
+  const char* forced = getenv("NMSPMM_FORCE_MX_BN");  // tests and sweeps
+  const int forced_bn = forced && *forced ? atoi(forced) : 0;
   int slot = 0;
   double best = 1e300;
   for (int i = 0; i < 3; ++i) {
+    if (forced_bn && kMxTiles[i] != forced_bn) continue;
     const int64_t units = n_mt * ((h->mx_rows + kMxTiles[i] - 1) / kMxTiles[i]);
     const double cost = (double)((units + pairs - 1) / pairs) * (kMxTiles[i] + 64);
     if (cost < best) {
@@ -714,31 +729,13 @@ nm_status mx_product(const nm_handle* h, const void* Q, const void* S, int64_t T
   if (units > INT32_MAX) return fail(NM_ERR_UNSUPPORTED, "T x n_out too large");
   a.units = (int)units;
 
-  CUtensorMap tmA, tmSA, tmY;
+  CUtensorMap tmA, tmSA;
   if ((st = codes_map(&tmA, Q, T, h->k, 128)) != NM_OK) return st;
   if ((st = scales_map(&tmSA, S, (int64_t)sbytes)) != NM_OK) return st;
-  a.tma_store = (n_y * es) % 16 == 0 ? 1 : 0;  // a tensor store needs a row pitch of whole 16-byte pieces
-  if (a.tma_store) {
-    const int cols = gated ? 16 : 32;
-    const uint64_t dims[2] = {(uint64_t)n_y, (uint64_t)T}, strides[1] = {(uint64_t)(n_y * es)};
-    const uint32_t box[2] = {(uint32_t)cols, 32};
-    const int rowb = cols * es;
-    st = encode_map(&tmY,
-                    a.out_ty == OUT_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                    : a.out_ty == OUT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                    2, Y, dims, strides, box,
-                    rowb == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                    : rowb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                 : CU_TENSOR_MAP_SWIZZLE_32B,
-                    CU_TENSOR_MAP_L2_PROMOTION_NONE);
-    if (st != NM_OK) return st;
-  } else {
-    tmY = tmA;  // not used
-  }
+  a.vec = (n_y * es) % 16 == 0 ? 1 : 0;
   const int grid = (int)(units < pairs ? units : pairs);
-  cudaError_t e = gated ? launch_mx<true>(h, slot, grid, tmA, tmSA, tmY, a, (cudaStream_t)stream)
-                        : launch_mx<false>(h, slot, grid, tmA, tmSA, tmY, a, (cudaStream_t)stream);
+  cudaError_t e = gated ? launch_mx<true>(h, slot, grid, tmA, tmSA, a, (cudaStream_t)stream)
+                        : launch_mx<false>(h, slot, grid, tmA, tmSA, a, (cudaStream_t)stream);
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "launch the microscaled product");
 }
 

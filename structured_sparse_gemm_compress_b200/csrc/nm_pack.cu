@@ -448,19 +448,13 @@ __global__ void __launch_bounds__(256) decompress_kernel(const uint8_t* __restri
       unpack16<T>(*reinterpret_cast<const uint4*>(chunk + swz128(rr, kk)), comp);
     }
     const uint32_t meta = *reinterpret_cast<const uint16_t*>(chunk + kAtomBytes + meta_off16(DT, rr, kk));
-#pragma unroll
-    for (int c = 0; c < 16; ++c) out[c] = (T)0;
+    // positions of a group's two slots always differ; selects keep `out` in registers
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int nib = (meta >> (4 * j)) & 0xF;
       const int i0 = nib & 3, i1 = (nib >> 2) & 3;
-      out[4 * j + i0] = comp[2 * j];
-      if (i1 != i0) {
-        out[4 * j + i1] = comp[2 * j + 1];
-      } else if (ES == 1) {
-        out[4 * j + i0] = (T)((int)comp[2 * j] + (int)comp[2 * j + 1]);
-      }
-      // (equal 2-byte positions only occur for all-zero padding slots)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) out[4 * j + c] = c == i0 ? comp[2 * j] : c == i1 ? comp[2 * j + 1] : (T)0;
     }
   } else {
 #pragma unroll
@@ -470,7 +464,15 @@ __global__ void __launch_bounds__(256) decompress_kernel(const uint8_t* __restri
                   out + h * (16 / ES));
     }
   }
-  for (int c = 0; c < valid; ++c) Wout[r * K + k0 + c] = out[c];
+  T* dst = Wout + r * K + k0;
+  if (valid == 16 && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
+#pragma unroll
+    for (int h = 0; h < ES; ++h) reinterpret_cast<uint4*>(dst)[h] = pack16<T>(out + h * (16 / ES));
+  } else {
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      if (c < valid) dst[c] = out[c];
+  }
 }
 
 // ------------------------------------------------------------------ tile-shared patterns

@@ -1,8 +1,10 @@
 // nm_stage.cuh -- output staging of the kernels whose accumulator lanes are
-// output rows: each thread of a warp holds a run of one row's columns; the warp's
-// 32 rows go through a small swizzled buffer in shared memory and leave as one
-// tensor store (or, where the row pitch rules that out, as plain stores along
-// the rows).
+// output rows: each thread of a warp holds a run of one row's columns.  The warp's
+// 32 rows go through a small swizzled buffer in shared memory and leave as
+// 16-byte stores along the rows, so that a warp instruction writes whole 128-byte
+// lines.  (Measured on the 4-bit product, 12608 x 4096 bf16 output: the same
+// tile leaving by tensor stores of 64-byte rows took 5-6 cycles a row and bound
+// the kernel at 34 us whatever its k.)
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -13,14 +15,13 @@ namespace nm {
 
 __host__ __device__ constexpr int stage_elem_bytes(int ot) { return ot == OUT_F32 ? 4 : 2; }
 
-// Byte offset of 16-byte piece c of row `row` in a staged tile with rows of
-// ROWB bytes: the tensor store's swizzle of that width (address bits 4.. of a
-// 16-byte piece XOR bits 7..), which also spreads a warp's 16-byte writes over
-// all banks (rows of 32 bytes: two per bank).
+// Byte offset of 16-byte piece c of row `row` in a staged tile with rows of ROWB
+// bytes: pieces are permuted within a row so that neither a thread's writes of its
+// own row nor the reads along the rows meet in a bank.
 template <int ROWB>
 __device__ __forceinline__ uint32_t stage_off(uint32_t row, uint32_t c) {
-  static_assert(ROWB == 128 || ROWB == 64 || ROWB == 32, "swizzle widths");
-  const uint32_t x = ROWB == 128 ? (row & 7u) : ROWB == 64 ? ((row >> 1) & 3u) : ((row >> 2) & 1u);
+  static_assert(ROWB == 128 || ROWB == 64, "staged row widths");
+  const uint32_t x = ROWB == 128 ? (row & 7u) : ((row >> 1) & 3u);
   return row * (uint32_t)ROWB + ((c ^ x) << 4);
 }
 
@@ -35,12 +36,11 @@ __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
   }
 }
 
-// NV values of this thread's row into the staged tile.
-template <int OT, int NV>
-__device__ __forceinline__ void stage_row(uint8_t* buf, uint32_t row, const float* v) {
-  constexpr int ROWB = NV * stage_elem_bytes(OT);
+// NV values of this thread's row into the staged tile, from 16-byte piece c0 on.
+template <int OT, int ROWB, int NV>
+__device__ __forceinline__ void stage_row(uint8_t* buf, uint32_t row, uint32_t c0, const float* v) {
 #pragma unroll
-  for (int c = 0; c < ROWB / 16; ++c) {
+  for (int c = 0; c < NV * stage_elem_bytes(OT) / 16; ++c) {
     uint4 q;
     if constexpr (OT == OUT_F32) {
       q = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
@@ -49,25 +49,43 @@ __device__ __forceinline__ void stage_row(uint8_t* buf, uint32_t row, const floa
       q = make_uint4(pack_pair<OT>(v[8 * c], v[8 * c + 1]), pack_pair<OT>(v[8 * c + 2], v[8 * c + 3]),
                      pack_pair<OT>(v[8 * c + 4], v[8 * c + 5]), pack_pair<OT>(v[8 * c + 6], v[8 * c + 7]));
     }
-    *reinterpret_cast<uint4*>(buf + stage_off<ROWB>(row, (uint32_t)c)) = q;
+    *reinterpret_cast<uint4*>(buf + stage_off<ROWB>(row, c0 + (uint32_t)c)) = q;
   }
 }
 
-// The staged tile's first `rows` rows and `cols` columns to y (row pitch ld
-// elements) by plain stores, neighbouring lanes on neighbouring columns.
-template <int OT, int NV>
-__device__ __forceinline__ void stage_copy_rows(const uint8_t* buf, void* y, int64_t ld, int rows, int cols,
-                                                int lane) {
-  constexpr int ES = stage_elem_bytes(OT), ROWB = NV * ES, PER = 16 / ES, RPI = 32 / NV;
-  const int col = lane % NV;
-  for (int r = lane / NV; r < rows; r += RPI) {
-    const uint8_t* src = buf + stage_off<ROWB>((uint32_t)r, (uint32_t)(col / PER)) + (col % PER) * ES;
-    if (col < cols) {
-      if constexpr (ES == 4)
-        reinterpret_cast<uint32_t*>(y)[r * ld + col] = *reinterpret_cast<const uint32_t*>(src);
-      else
-        reinterpret_cast<uint16_t*>(y)[r * ld + col] = *reinterpret_cast<const uint16_t*>(src);
+// The staged tile's first `rows` rows, `bytes` of each, to y (row pitch in bytes).
+// vec: y and the pitch are multiples of 16 bytes, and so is `bytes`.  es: element
+// bytes of the other case.
+template <int ROWB>
+__device__ __forceinline__ void stage_flush(const uint8_t* buf, uint8_t* y, int64_t pitch, int rows, int bytes, bool vec,
+                                            int es, int lane) {
+  if (vec) {
+    constexpr int PER = ROWB / 16, RPI = 32 / PER;  // lanes per row, rows per instruction
+    const int c = lane % PER;
+    uint8_t* dst = y + (int64_t)(lane / PER) * pitch + c * 16;
+    if (rows >= 32 && bytes >= ROWB) {
+#pragma unroll
+      for (int r = 0; r < 32; r += RPI) {
+        const uint4 q = *reinterpret_cast<const uint4*>(buf + stage_off<ROWB>((uint32_t)(r + lane / PER), (uint32_t)c));
+        *reinterpret_cast<uint4*>(dst + (int64_t)r * pitch) = q;
+      }
+    } else {
+#pragma unroll 1
+      for (int r = lane / PER; r < rows; r += RPI)
+        if (c * 16 < bytes)
+          *reinterpret_cast<uint4*>(y + (int64_t)r * pitch + c * 16) =
+              *reinterpret_cast<const uint4*>(buf + stage_off<ROWB>((uint32_t)r, (uint32_t)c));
     }
+  } else {  // neighbouring lanes on neighbouring elements of one row
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r)
+      for (int b = lane * es; b < bytes; b += 32 * es) {
+        const uint8_t* src = buf + stage_off<ROWB>((uint32_t)r, (uint32_t)(b >> 4)) + (b & 15);
+        if (es == 4)
+          *reinterpret_cast<uint32_t*>(y + (int64_t)r * pitch + b) = *reinterpret_cast<const uint32_t*>(src);
+        else
+          *reinterpret_cast<uint16_t*>(y + (int64_t)r * pitch + b) = *reinterpret_cast<const uint16_t*>(src);
+      }
   }
 }
 
