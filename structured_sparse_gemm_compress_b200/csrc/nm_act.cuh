@@ -109,9 +109,40 @@ __device__ __forceinline__ void gelu2(float& x0, float& x1) {
 // reciprocal to 1 ulp; a power that overflows gives 0, one that vanishes gives x.
 constexpr float kLog2e = 1.4426950409f;
 __device__ __forceinline__ float sigmoid1(float x) { return rcp_approx(__fadd_rn(1.0f, ex2_approx(__fmul_rn(x, -kLog2e)))); }
-__device__ __forceinline__ float silu1(float x) { return __fmul_rn(x, sigmoid1(x)); }
 // max(x, 0) that lets a NaN through.
 __device__ __forceinline__ float relu1(float x) { return x < 0.0f ? 0.0f : x; }
+
+// The same GELU in fewer instructions, for the outputs of the gated and the
+// microscaled products: with q as above, GELU(x) = max(x, 0) - |x| q, one fused
+// multiply-add where gelu2 takes a subtraction, two selections and a product
+// (9 instructions a value instead of 11.5).  Not bit-identical to gelu2, whose
+// results the older output stages keep; the same error bound.
+__device__ __forceinline__ void gelu2_relu_form(float& x0, float& x1) {
+  using namespace gelu_as;
+  const uint64_t na = pk2(-fabsf(x0), -fabsf(x1));
+  float d0, d1;
+  upk2(fma2(na, pk2(-kP, -kP), pk2(1.0f, 1.0f)), d0, d1);
+  const uint64_t t = pk2(rcp_approx(d0), rcp_approx(d1));
+  uint64_t h = fma2(t, pk2(kB5, kB5), pk2(kB4, kB4));
+  h = fma2(t, h, pk2(kB3, kB3));
+  h = fma2(t, h, pk2(kB2, kB2));
+  h = fma2(t, h, pk2(kB1, kB1));
+  h = mul2(t, h);
+  float w0, w1;
+  upk2(mul2(na, mul2(na, pk2(kE, kE))), w0, w1);
+  const uint64_t q = mul2(h, pk2(ex2_approx(w0), ex2_approx(w1)));
+  upk2(fma2(na, q, pk2(fmaxf(x0, 0.0f), fmaxf(x1, 0.0f))), x0, x1);
+}
+
+// SiLU of a pair.
+__device__ __forceinline__ void silu2(float& x0, float& x1) {
+  const uint64_t x = pk2(x0, x1);
+  float w0, w1;
+  upk2(mul2(x, pk2(-kLog2e, -kLog2e)), w0, w1);
+  float d0, d1;
+  upk2(add2(pk2(ex2_approx(w0), ex2_approx(w1)), pk2(1.0f, 1.0f)), d0, d1);
+  upk2(mul2(x, pk2(rcp_approx(d0), rcp_approx(d1))), x0, x1);
+}
 
 // act(x) of N values, one uniform branch around each activation's loop.
 template <int N>
@@ -119,10 +150,10 @@ __device__ __forceinline__ void act_run(float* x, int act) {
   static_assert(N % 2 == 0, "values go in pairs");
   if (act == ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < N; i += 2) gelu2(x[i], x[i + 1]);
+    for (int i = 0; i < N; i += 2) gelu2_relu_form(x[i], x[i + 1]);
   } else if (act == ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = silu1(x[i]);
+    for (int i = 0; i < N; i += 2) silu2(x[i], x[i + 1]);
   } else if (act == ACT_RELU) {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = relu1(x[i]);

@@ -270,6 +270,12 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t local_addr, uint32_t ra
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// The same without a release: for a barrier that guards tensor memory which the
+// arriving warp has finished reading (tcgen05.wait::ld) and no other memory.  A
+// release would first wait for the lane's own output stores to become visible.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // 2-D tensor copy of a CTA pair (no multicast): data lands in this CTA's shared
 // memory, completion bytes are counted on the mbarrier at `bar_cluster_addr`
 // (the pair leader's barrier).

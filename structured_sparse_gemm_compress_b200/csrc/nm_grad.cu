@@ -263,7 +263,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
   __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
   __shared__ __align__(8) uint64_t accf_bar[2];
   __shared__ __align__(8) uint64_t acce_bar[2];
-  __shared__ __align__(8) uint64_t pfree_bar[2];  // peer: its epilogue warps have read accumulator i
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_sh;
@@ -278,8 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&accf_bar[i], 1);
-      mbar_init(&acce_bar[i], kGradEpiWarps + 1);  // the leader's epilogue warps, and one arrive for all the peer's
-      mbar_init(&pfree_bar[i], kGradEpiWarps);
+      mbar_init(&acce_bar[i], 2 * kGradEpiWarps);  // both CTAs' epilogue warps
     }
     mbar_init(&drain_bar, 1);
     abort_sh = 0;
@@ -396,24 +394,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         }
       }
       if (issuer) tc_commit_pair(&drain_bar, (uint16_t)3);
-    } else {
-      // Peer: turn each accumulator release of this CTA's epilogue warps into one
-      // cluster-scope arrive on the leader (theirs would first wait for their own
-      // output stores to become visible; this warp has none in flight).
-      const bool issuer = elect_one();
-      int acc = 0;
-      uint32_t acc_phase = 0;
-      for (int i = 0; grad_unit(a, pair, pairs, i, BN, u); ++i) {
-        if (!mbar_wait_warp(&pfree_bar[acc], acc_phase, &abort_sh, tmo)) {
-          if (issuer) give_up(4);
-          break;
-        }
-        if (issuer) mbar_arrive_cluster(acce_lead0 + 8u * (uint32_t)acc);
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
-      }
     }
     mbar_wait_warp(&drain_bar, 0, &abort_sh, tmo);  // every MMA of this pair has completed
   } else {
@@ -442,10 +422,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
           __syncwarp();
           tmem_ld32(taddr + (uint32_t)(c + 32 * h), r);
           tmem_wait_ld();
-          if (h == 1 && c + 64 == C::WCOLS) {  // the peer's release is forwarded by its warp 1
+          if (h == 1 && c + 64 == C::WCOLS) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(leader ? &acce_bar[acc] : &pfree_bar[acc]);
+            if (lane == 0) mbar_arrive_cluster_relaxed(acce_lead0 + 8u * (uint32_t)acc);
           }
           float v[32];
 #pragma unroll
@@ -454,8 +434,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         }
         __syncwarp();
         if (rows > 0 && col0 + c < a.k)
-          stage_flush<128>(buf, out + (int64_t)(col0 + c) * 2, (int64_t)a.k * 2, rows, min(64, a.k - col0 - c) * 2, true, 2,
-                           lane);
+          stage_flush<128, 2>(buf, out + (int64_t)(col0 + c) * 2, (int64_t)a.k * 2, rows, min(64, a.k - col0 - c) * 2,
+                              true, lane);
         __syncwarp();
       }
       if (++acc == 2) {

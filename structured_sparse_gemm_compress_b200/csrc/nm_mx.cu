@@ -256,28 +256,31 @@ cudaError_t launch_dequantize(const uint8_t* Q, const uint8_t* S, int64_t rows, 
 // What bounds it: at k = 1024 the output's bytes (4 stages of 512 cycles feed a
 // tile whose stores take longer); at long k the tensor pipe.
 constexpr int kMxKb = 256;
-constexpr int kMxSmemBudget = 227 * 1024 - 1024;
+constexpr int kMxSmemBudget = 227 * 1024 - 1024 - 512;  // 1 KB of alignment slack, barriers
 
-template <int BN>
+template <int BN, bool GATED>
 struct MxCfg {
   static constexpr int HB = BN / 2;                            // channel rows each CTA loads
   static constexpr int ATOMS = BN > 128 ? 2 : 1;               // 128-channel scale tiles that cover BN channels
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int B_BYTES = HB * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES + 1024 + ATOMS * 1024;
-  // epilogue warps per lane quarter: 64 (BN = 64: 32) accumulator columns each
-  static constexpr int EPW = BN == 192 ? 3 : 2;
+  // Accumulator columns per epilogue warp: 32, or 64 for gated tiles (32 outputs,
+  // a 64-byte run of a 16-bit row).  12608 x 1024 -> 4096 with bias and GELU took
+  // 53.7 us with 32 columns a warp (24 warps of 72 registers) and 57.8 with 64.
+  static constexpr int WCOLS = GATED && BN > 64 ? 64 : 32;
+  static constexpr int EPW = BN / WCOLS;                       // epilogue warps per lane quarter
   static constexpr int EPI_WARPS = 4 * EPW;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-  static constexpr int EPI_BUF = 4096;                         // per warp: 32 staged rows of up to 128 bytes
+  static constexpr int EPI_BUF = 2048;                         // per warp: 32 staged rows of 64 bytes
   static constexpr int EPI_BYTES = EPI_WARPS * EPI_BUF;
-  static constexpr int STAGES_FIT = (kMxSmemBudget - EPI_BYTES) / STAGE;
+  static constexpr int VEC_BYTES = EPI_WARPS * 2 * WCOLS * 4;  // (static) scale and bias of each warp's columns
+  static constexpr int STAGES_FIT = (kMxSmemBudget - EPI_BYTES - VEC_BYTES) / STAGE;
   static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
   static constexpr int SMEM = STAGES * STAGE + EPI_BYTES + 1024;
   static constexpr int SF_COLS = 8 + 8 * ATOMS;                // scale columns of one stage
   static constexpr int COLS_NEEDED = 2 * BN + 2 * SF_COLS;
   static constexpr int TMEM_COLS = COLS_NEEDED <= 256 ? 256 : 512;
-  static constexpr int WCOLS = BN / EPW;                       // accumulator columns per epilogue warp
   static_assert(STAGE % 1024 == 0 && B_BYTES % 1024 == 0, "stages keep 1024-byte alignment");
   static_assert(STAGES >= 3 && COLS_NEEDED <= 512 && WCOLS % 32 == 0, "tile fits");
   // a tile starts at a multiple of BN: 64 rows into a scale tile at most
@@ -305,23 +308,14 @@ __host__ __device__ constexpr uint32_t mx_idesc(uint32_t sf_id) {
          (sf_id << 29);
 }
 
-// The output stage's share of one epilogue warp: WCOLS accumulator columns of its
-// 32 tokens, 32 at a time: scale, bias, activation (and gate), then staged rows
-// of up to 128 bytes.  `release` runs once the last columns are in registers.
-template <int OT, int WCOLS, bool GATED, typename Release>
-__device__ __forceinline__ void mx_epilogue(const MxArgs& a, uint32_t taddr, uint8_t* buf, float* vs, float* vb, int row0,
-                                            int col0, int lane, Release release) {
-  constexpr int ES = stage_elem_bytes(OT);
-  constexpr int NV = GATED ? 16 : 32;                         // outputs of one step
-  constexpr int OUTB = WCOLS / 32 * NV * ES;                  // output bytes of the warp's run of a row
-  constexpr int ROWB = OUTB >= 128 ? 128 : 64;                // (half of a 64-byte row stays unused at 32)
-  constexpr int STEPS = ROWB / (NV * ES) < WCOLS / 32 ? ROWB / (NV * ES) : WCOLS / 32;  // steps per staged tile
-  const int rows = min(32, a.T - row0);
+// Scale and bias of a warp's accumulator columns, one column of every 32 per lane.
+template <int WCOLS, bool GATED>
+struct MxVectors {
+  float s[WCOLS / 32], b[WCOLS / 32];
+  __device__ __forceinline__ void fetch(const MxArgs& a, int col0, int lane) {
 #pragma unroll
-  for (int c = 0; c < WCOLS / 32; ++c) {
-    const int col = col0 + 32 * c;
-    if (a.scale || a.bias) {  // this lane fetches the values of one accumulator column
-      const int ch = col + lane;
+    for (int c = 0; c < WCOLS / 32; ++c) {
+      const int ch = col0 + 32 * c + lane;
       int src = ch;
       bool in = ch < a.n_acc;
       if constexpr (GATED) {
@@ -329,66 +323,87 @@ __device__ __forceinline__ void mx_epilogue(const MxArgs& a, uint32_t taddr, uin
         in = f < a.n_ff;
         src = (ch & 16) ? a.n_ff + f : f;
       }
-      __syncwarp();
-      if (a.scale) vs[lane] = in ? __ldg(a.scale + src) : 0.0f;
-      if (a.bias) vb[lane] = in ? __ldg(a.bias + src) : 0.0f;
-    }
-    uint32_t r[32];
-    __syncwarp();
-    tmem_ld32(taddr + 32u * c, r);
-    tmem_wait_ld();
-    if (c == WCOLS / 32 - 1) release();
-    float v[32];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-    if (a.scale) {
-#pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 s4 = *reinterpret_cast<const float4*>(vs + j);
-        upk2(mul2(pk2(v[j], v[j + 1]), pk2(s4.x, s4.y)), v[j], v[j + 1]);
-        upk2(mul2(pk2(v[j + 2], v[j + 3]), pk2(s4.z, s4.w)), v[j + 2], v[j + 3]);
-      }
-    }
-    if (a.bias) {
-#pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 b4 = *reinterpret_cast<const float4*>(vb + j);
-        upk2(add2(pk2(v[j], v[j + 1]), pk2(b4.x, b4.y)), v[j], v[j + 1]);
-        upk2(add2(pk2(v[j + 2], v[j + 3]), pk2(b4.z, b4.w)), v[j + 2], v[j + 3]);
-      }
-    }
-    act_run<NV>(v, a.act);
-    if constexpr (GATED) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], v[j + 16]);
-    }
-    stage_row<OT, ROWB, NV>(buf, (uint32_t)lane, (uint32_t)((c % STEPS) * NV * ES / 16), v);
-    if (c % STEPS == STEPS - 1) {
-      const int ycol = (GATED ? col0 / 2 : col0) + (c - (STEPS - 1)) * NV;
-      __syncwarp();
-      if (rows > 0 && ycol < a.n_y)
-        stage_flush<ROWB>(buf, static_cast<uint8_t*>(a.Y) + ((int64_t)row0 * a.n_y + ycol) * ES, (int64_t)a.n_y * ES,
-                          rows, min(STEPS * NV, a.n_y - ycol) * ES, a.vec != 0, ES, lane);
-      __syncwarp();
+      s[c] = a.scale && in ? __ldg(a.scale + src) : 0.0f;
+      b[c] = a.bias && in ? __ldg(a.bias + src) : 0.0f;
     }
   }
+  // Into shared memory, where every lane reads them all.
+  __device__ __forceinline__ void publish(const MxArgs& a, float* vs, float* vb, int lane) const {
+    if (!a.scale && !a.bias) return;
+    __syncwarp();  // the previous tile's reads are done
+#pragma unroll
+    for (int c = 0; c < WCOLS / 32; ++c) {
+      vs[32 * c + lane] = s[c];
+      vb[32 * c + lane] = b[c];
+    }
+    __syncwarp();
+  }
+};
+
+// The output stage of one epilogue warp: WCOLS accumulator columns of its 32
+// tokens, all in registers (v).  32 columns at a time: scale, bias, activation
+// (and gate), then staged rows of 64 bytes.
+template <int OT, int WCOLS, bool GATED>
+__device__ __forceinline__ void mx_epilogue(const MxArgs& a, float (&v)[WCOLS], uint8_t* buf, const float* vs,
+                                            const float* vb, int row0, int col0, int lane) {
+  constexpr int ES = stage_elem_bytes(OT);
+  constexpr int NV = GATED ? 16 : 32;            // outputs of one step of 32 columns
+  constexpr int PER = 64 / ES;                   // outputs of a staged row
+  constexpr int TOTAL = WCOLS / 32 * NV;         // outputs of this warp per token
+  const int rows = min(32, a.T - row0);
+  if (a.scale) {
+#pragma unroll
+    for (int j = 0; j < WCOLS; j += 4) {
+      const float4 s4 = *reinterpret_cast<const float4*>(vs + j);
+      upk2(mul2(pk2(v[j], v[j + 1]), pk2(s4.x, s4.y)), v[j], v[j + 1]);
+      upk2(mul2(pk2(v[j + 2], v[j + 3]), pk2(s4.z, s4.w)), v[j + 2], v[j + 3]);
+    }
+  }
+  if (a.bias) {
+#pragma unroll
+    for (int j = 0; j < WCOLS; j += 4) {
+      const float4 b4 = *reinterpret_cast<const float4*>(vb + j);
+      upk2(add2(pk2(v[j], v[j + 1]), pk2(b4.x, b4.y)), v[j], v[j + 1]);
+      upk2(add2(pk2(v[j + 2], v[j + 3]), pk2(b4.z, b4.w)), v[j + 2], v[j + 3]);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < WCOLS / 32; ++c) {
+    act_run<NV>(v + 32 * c, a.act);
+    if constexpr (GATED) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[16 * c + j] = __fmul_rn(v[32 * c + j], v[32 * c + 16 + j]);
+    }
+  }
+  // outputs v[0 .. TOTAL)
+#pragma unroll
+  for (int o = 0; o < TOTAL; o += PER) {
+    constexpr int N = TOTAL < PER ? TOTAL : PER;
+    if (o > 0) __syncwarp();
+    stage_row<OT, 64, N>(buf, (uint32_t)lane, 0, v + o);
+    __syncwarp();
+    const int ycol = (GATED ? col0 / 2 : col0) + o;
+    if (rows > 0 && ycol < a.n_y)
+      stage_flush<64, ES>(buf, static_cast<uint8_t*>(a.Y) + ((int64_t)row0 * a.n_y + ycol) * ES, (int64_t)a.n_y * ES, rows,
+                      min(N, a.n_y - ycol) * ES, a.vec != 0, lane);
+  }
+  __syncwarp();
 }
 
 template <int BN, bool GATED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxCfg<BN>::THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxCfg<BN, GATED>::THREADS, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                    const MxArgs a) {
-  using C = MxCfg<BN>;
+  using C = MxCfg<BN, GATED>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full_bar[C::STAGES];
   __shared__ __align__(8) uint64_t empty_bar[C::STAGES];
   __shared__ __align__(8) uint64_t accf_bar[2];
   __shared__ __align__(8) uint64_t acce_bar[2];
-  __shared__ __align__(8) uint64_t pfree_bar[2];  // peer: its epilogue warps have read accumulator i
   __shared__ __align__(8) uint64_t drain_bar;
-  __shared__ __align__(16) float vec_sh[C::EPI_WARPS][2][32];
+  __shared__ __align__(16) float vec_sh[C::EPI_WARPS][2][C::WCOLS];
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_sh;
 
@@ -402,8 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxCfg<BN>::THREADS, 
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&accf_bar[i], 1);
-      mbar_init(&acce_bar[i], C::EPI_WARPS + 1);  // the leader's epilogue warps, and one arrive for all the peer's
-      mbar_init(&pfree_bar[i], C::EPI_WARPS);
+      mbar_init(&acce_bar[i], 2 * C::EPI_WARPS);  // both CTAs' epilogue warps
     }
     mbar_init(&drain_bar, 1);
     abort_sh = 0;
@@ -536,24 +550,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxCfg<BN>::THREADS, 
         }
       }
       if (issuer) tc_commit_pair(&drain_bar, (uint16_t)3);
-    } else {
-      // Peer: turn each accumulator release of this CTA's epilogue warps into one
-      // cluster-scope arrive on the leader (theirs would first wait for their own
-      // output stores to become visible; this warp has none in flight).
-      const bool issuer = elect_one();
-      int acc = 0;
-      uint32_t acc_phase = 0;
-      for (int u = u_first; u < a.units; u += u_step) {
-        if (!mbar_wait_warp(&pfree_bar[acc], acc_phase, &abort_sh, tmo)) {
-          if (issuer) give_up(4);
-          break;
-        }
-        if (issuer) mbar_arrive_cluster(acce_lead0 + 8u * (uint32_t)acc);
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
-      }
     }
     mbar_wait_warp(&drain_bar, 0, &abort_sh, tmo);  // every MMA of this pair has completed
   } else {
@@ -564,25 +560,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxCfg<BN>::THREADS, 
     float* vb = vec_sh[ew][1];
     int acc = 0;
     uint32_t acc_phase = 0;
+    MxVectors<C::WCOLS, GATED> vec;  // of the next tile: fetched a tile ahead
+    vec.fetch(a, (u_first % a.n_nt) * BN + part * C::WCOLS, lane);
     for (int u = u_first; u < a.units; u += u_step) {
       const int nt = u % a.n_nt, mt = u / a.n_nt;
+      const int row0 = mt * 256 + (int)rank * 128 + lq * 32;
+      const int col0 = nt * BN + part * C::WCOLS;
+      vec.publish(a, vs, vb, lane);
+      vec.fetch(a, ((u + u_step) % a.n_nt) * BN + part * C::WCOLS, lane);
       if (!mbar_wait_warp(&accf_bar[acc], acc_phase, &abort_sh, tmo)) {
         if (lane == 0) give_up(4);
         break;
       }
       tc_fence_after();
-      const int row0 = mt * 256 + (int)rank * 128 + lq * 32;
-      const int col0 = nt * BN + part * C::WCOLS;
       const uint32_t taddr = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * BN + part * C::WCOLS);
-      auto release = [&]() {  // the peer's release is forwarded by its warp 1
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(leader ? &acce_bar[acc] : &pfree_bar[acc]);
-      };
+      float v[C::WCOLS];
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < C::WCOLS; c += 32) tmem_ld32(taddr + (uint32_t)c, *reinterpret_cast<uint32_t(*)[32]>(v + c));
+      tmem_wait_ld();
+      // all of this warp's columns are in registers: release the accumulator
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(acce_lead0 + 8u * (uint32_t)acc);
       switch (a.out_ty) {
-        case OUT_F16: mx_epilogue<OUT_F16, C::WCOLS, GATED>(a, taddr, buf, vs, vb, row0, col0, lane, release); break;
-        case OUT_BF16: mx_epilogue<OUT_BF16, C::WCOLS, GATED>(a, taddr, buf, vs, vb, row0, col0, lane, release); break;
-        default: mx_epilogue<OUT_F32, C::WCOLS, GATED>(a, taddr, buf, vs, vb, row0, col0, lane, release); break;
+        case OUT_F16: mx_epilogue<OUT_F16, C::WCOLS, GATED>(a, v, buf, vs, vb, row0, col0, lane); break;
+        case OUT_BF16: mx_epilogue<OUT_BF16, C::WCOLS, GATED>(a, v, buf, vs, vb, row0, col0, lane); break;
+        default: mx_epilogue<OUT_F32, C::WCOLS, GATED>(a, v, buf, vs, vb, row0, col0, lane); break;
       }
       if (++acc == 2) {
         acc = 0;
@@ -606,7 +610,7 @@ constexpr int kMxTiles[3] = {192, 128, 64};
 template <int BN, bool GATED>
 cudaError_t launch_mx_t(const nm_handle* h, int slot, int grid, const CUtensorMap& tmA, const CUtensorMap& tmSA,
                         const MxArgs& a, cudaStream_t s) {
-  using C = MxCfg<BN>;
+  using C = MxCfg<BN, GATED>;
   auto kern = mx_pair_kernel<BN, GATED>;
   static std::atomic<uint64_t> opted{0};
   cudaError_t e = smem_opt_in(kern, C::SMEM, opted);

@@ -54,11 +54,11 @@ __device__ __forceinline__ void stage_row(uint8_t* buf, uint32_t row, uint32_t c
 }
 
 // The staged tile's first `rows` rows, `bytes` of each, to y (row pitch in bytes).
-// vec: y and the pitch are multiples of 16 bytes, and so is `bytes`.  es: element
-// bytes of the other case.
-template <int ROWB>
+// vec: y and the pitch are multiples of 16 bytes, and so is `bytes`; otherwise
+// elements of ES bytes go one by one.
+template <int ROWB, int ES>
 __device__ __forceinline__ void stage_flush(const uint8_t* buf, uint8_t* y, int64_t pitch, int rows, int bytes, bool vec,
-                                            int es, int lane) {
+                                            int lane) {
   if (vec) {
     constexpr int PER = ROWB / 16, RPI = 32 / PER;  // lanes per row, rows per instruction
     const int c = lane % PER;
@@ -77,15 +77,21 @@ __device__ __forceinline__ void stage_flush(const uint8_t* buf, uint8_t* y, int6
               *reinterpret_cast<const uint4*>(buf + stage_off<ROWB>((uint32_t)r, (uint32_t)c));
     }
   } else {  // neighbouring lanes on neighbouring elements of one row
-#pragma unroll 1
-    for (int r = 0; r < rows; ++r)
-      for (int b = lane * es; b < bytes; b += 32 * es) {
+    constexpr int PER = ROWB / ES < 32 ? ROWB / ES : 32, RPI = 32 / PER;  // lanes per row, rows per instruction
+#pragma unroll 4
+    for (int r = lane / PER; r < rows; r += RPI) {
+#pragma unroll
+      for (int e = 0; e < ROWB; e += PER * ES) {
+        const int b = e + (lane % PER) * ES;
         const uint8_t* src = buf + stage_off<ROWB>((uint32_t)r, (uint32_t)(b >> 4)) + (b & 15);
-        if (es == 4)
-          *reinterpret_cast<uint32_t*>(y + (int64_t)r * pitch + b) = *reinterpret_cast<const uint32_t*>(src);
-        else
-          *reinterpret_cast<uint16_t*>(y + (int64_t)r * pitch + b) = *reinterpret_cast<const uint16_t*>(src);
+        if (b < bytes) {
+          if constexpr (ES == 4)
+            *reinterpret_cast<uint32_t*>(y + (int64_t)r * pitch + b) = *reinterpret_cast<const uint32_t*>(src);
+          else
+            *reinterpret_cast<uint16_t*>(y + (int64_t)r * pitch + b) = *reinterpret_cast<const uint16_t*>(src);
+        }
       }
+    }
   }
 }
 
