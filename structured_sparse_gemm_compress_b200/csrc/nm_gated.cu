@@ -14,12 +14,16 @@ cudaError_t launch_img(const CUtensorMap* tmX, const CUtensorMap* tmW, const Pla
   // the output never leaves by tensor stores: its map argument is not read
   if (p.xkb > 0 || (p.splits > 1 && !p.cluster)) return cudaErrorInvalidValue;
   if (p.pair) {
-    switch (p.bn) {
-      case 128: return launch_pair_t<DT, IMG, 128, kOut>(tmX, tmX, tmW, p, a, s);
-      case 192: return launch_pair_t<DT, IMG, 192, kOut>(tmX, tmX, tmW, p, a, s);
-      case 224: return launch_pair_t<DT, IMG, 224, kOut>(tmX, tmX, tmW, p, a, s);
-      default: return cudaErrorInvalidValue;
+    if constexpr (DT != DT_I8) {
+      if (a.P && a.n_ff % 8 == 0) {  // every row of p starts on 16 bytes
+        if (p.bn == 192) return launch_pair_t<DT, IMG, 192, kOut | kOutSave>(tmX, tmX, tmW, p, a, s);
+        if (p.bn == 128) return launch_pair_t<DT, IMG, 128, kOut | kOutSave>(tmX, tmX, tmW, p, a, s);
+        return cudaErrorInvalidValue;
+      }
     }
+    if (p.bn == 192) return launch_pair_t<DT, IMG, 192, kOut>(tmX, tmX, tmW, p, a, s);
+    if (p.bn == 128) return launch_pair_t<DT, IMG, 128, kOut>(tmX, tmX, tmW, p, a, s);
+    return cudaErrorInvalidValue;
   }
   switch (p.bn) {
     case 32: return launch_t<DT, IMG, 32, kOut, 0>(tmX, tmX, tmW, p, a, s);

@@ -12,12 +12,14 @@
 // core reads MN-major operands as well, so nothing is transposed: tensor copies
 // bring 64-wide runs of the kept axis, 64 summed rows each.
 #include <algorithm>
+#include <cstdlib>
 
 #include "nm_act.cuh"
 #include "nm_api_internal.h"
 #include "nm_device.cuh"
 #include "nm_launch.cuh"
 #include "nm_stage.cuh"
+#include "nm_unpack.cuh"
 
 namespace nm {
 namespace {
@@ -25,7 +27,6 @@ namespace {
 // ------------------------------------------------------------------ dp and dbias
 
 constexpr int kDpCols = 256;  // columns of each half per block
-constexpr int kDpRows = 128;  // rows per block
 constexpr int kDpWarps = 8;
 
 template <int DT>
@@ -80,6 +81,15 @@ __device__ __forceinline__ void dp_store(uint16_t* row, int f0, int F, int lane,
   }
 }
 
+// The masked dense weight, unpacked by the first blocks of the same launch (dX
+// reads it with dp): Wm null or blocks = 0 when dX is not asked for.
+struct UnpackArgs {
+  const uint8_t* bpack;
+  uint16_t* Wm;
+  long long units, K;
+  int img, n_kb, n_ff, blocks;
+};
+
 // One pass over P and dY: dp [T][2][pitch] in the handle's type (rounded for the
 // tensor core; columns n_ff .. pitch are never read) and, with `part`, the fp32
 // column sums of this block's rows ([row block][2][n_ff]), each warp's rows in
@@ -89,13 +99,23 @@ __device__ __forceinline__ void dp_store(uint16_t* row, int f0, int F, int lane,
 template <int DT, bool VEC, bool BIAS>
 __global__ void __launch_bounds__(32 * kDpWarps, BIAS ? 3 : 4)
     gated_dp_kernel(const uint16_t* __restrict__ P, const uint16_t* __restrict__ dY, int T, int F, int pitch, int act,
-                    uint16_t* __restrict__ dp, float* __restrict__ part) {
+                    uint16_t* __restrict__ dp, float* __restrict__ part, int block_rows, int col_blocks,
+                    const UnpackArgs un) {
   __shared__ float sums[BIAS ? kDpWarps : 1][2][kDpCols];
   pdl_launch_dependents();
   pdl_wait();
+  if ((int)blockIdx.x < un.blocks) {
+    const long long unit = (long long)blockIdx.x * (32 * kDpWarps) + threadIdx.x, per_row = (un.K + 15) / 16;
+    if (unit < un.units) {
+      const long long r = unit / per_row;
+      unpack_unit<DT>(un.bpack, un.n_ff, un.K, un.img, un.n_kb, un.Wm, r, (unit - r * per_row) * 16);
+    }
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int f0 = blockIdx.x * kDpCols, t0 = blockIdx.y * kDpRows;
-  const int t1 = min(T, t0 + kDpRows);
+  const int block = (int)blockIdx.x - un.blocks, row_block = block / col_blocks;
+  const int f0 = (block - row_block * col_blocks) * kDpCols, t0 = row_block * block_rows;
+  const int t1 = min(T, t0 + block_rows);
   float sg[8] = {}, su[8] = {};
   for (int t = t0 + warp; t < t1; t += kDpWarps) {
     const uint16_t* prow = P + (size_t)t * 2 * F;
@@ -130,28 +150,38 @@ __global__ void __launch_bounds__(32 * kDpWarps, BIAS ? 3 : 4)
       float s = 0.0f;
 #pragma unroll
       for (int w = 0; w < kDpWarps; ++w) s += sums[w][z][c];
-      if (f0 + c < F) part[((size_t)blockIdx.y * 2 + z) * F + f0 + c] = s;
+      if (f0 + c < F) part[((size_t)row_block * 2 + z) * F + f0 + c] = s;
     }
   }
 }
 
-// dbias [2 n_ff]: the row blocks' sums, eight interleaved runs of them per column, the runs in order.
-__global__ void __launch_bounds__(256) dbias_kernel(const float* __restrict__ part, int n, int blocks,
+// dbias: one warp adds up the row blocks' sums of 32 columns, as eight interleaved
+// runs (eight loads in flight) that are then added in order.
+__device__ __forceinline__ void dbias_columns(const float* __restrict__ part, int n, int row_blocks, int c,
+                                              float* __restrict__ dbias) {
+  if (c >= n) return;
+  float run[8] = {};
+  int b = 0;
+  for (; b + 8 <= row_blocks; b += 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) run[i] += __ldg(part + (size_t)(b + i) * n + c);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (b + i < row_blocks) run[i] += __ldg(part + (size_t)(b + i) * n + c);
+  float s = run[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) s += run[i];
+  dbias[c] = s;
+}
+
+// The launch of a call that asks for nothing else; otherwise the products' idle
+// epilogue warps do this before their first tile.
+__global__ void __launch_bounds__(128) dbias_kernel(const float* __restrict__ part, int n, int row_blocks,
                                                     float* __restrict__ dbias) {
-  __shared__ float sums[8][32];
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-  float s = 0.0f;
-  if (c < n)
-    for (int b = run; b < blocks; b += 8) s += part[(size_t)b * n + c];
-  sums[run][lane] = s;
-  __syncthreads();
-  if (run == 0 && c < n) {
-#pragma unroll
-    for (int r = 1; r < 8; ++r) s += sums[r][lane];
-    dbias[c] = s;
-  }
+  dbias_columns(part, n, row_blocks, (int)(blockIdx.x * blockDim.x + threadIdx.x), dbias);
 }
 
 // ------------------------------------------------------------------ the two products
@@ -199,6 +229,9 @@ struct GradArgs {
   int F, T, k;
   int kb_half;       // dX: stages per half of 2 n_ff
   void *dW, *dX;
+  const float* part;       // with dbias: the row blocks' column sums, row_blocks of them
+  float* dbias;
+  int row_blocks;
   int* err;
   unsigned long long timeout_ns;
 };
@@ -401,6 +434,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     constexpr int OT = DT == DT_F16 ? OUT_F16 : OUT_BF16;
     const int ew = warp - 2, lq = warp & 3, part = ew >> 2;
     uint8_t* buf = smem + (size_t)C::STAGES * C::STAGE + (size_t)ew * C::EPI_BUF;
+    if (a.dbias)  // while the first tile is summed
+      for (int c = ((int)blockIdx.x * kGradEpiWarps + ew) * 32; c < 2 * a.F; c += (int)gridDim.x * kGradEpiWarps * 32)
+        dbias_columns(a.part, 2 * a.F, a.row_blocks, c + lane, a.dbias);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int i = 0; grad_unit(a, pair, pairs, i, BN, u); ++i) {
@@ -467,15 +503,24 @@ cudaError_t launch_grad_t(int grid, const GradMaps& m, const GradArgs& a, cudaSt
   return launch_pdl(kern, dim3((unsigned)(2 * grid)), kGradThreads, GradCfg<BN>::SMEM, s, 0, m.pw, m.px, m.x, m.w, a);
 }
 
+// Rows per block: eight a warp, or two when that would leave SMs without a block
+// (1379 x 2 x 2051 with the bias: 18.6 us with 16 rows a warp, 11.1 with two).
+int dp_block_rows(int64_t T, int64_t F) {
+  const int64_t col_blocks = (F + kDpCols - 1) / kDpCols;
+  return (T + 63) / 64 * col_blocks >= 4 * 148 ? 64 : 16;
+}
+
 template <int DT>
 cudaError_t launch_dp(bool vec, const void* P, const void* dY, int T, int F, int pitch, int act, void* dp, float* part,
-                      cudaStream_t s) {
-  const dim3 grid((unsigned)((F + kDpCols - 1) / kDpCols), (unsigned)((T + kDpRows - 1) / kDpRows));
+                      const UnpackArgs& un, cudaStream_t s) {
+  const int rows = dp_block_rows(T, F), col_blocks = (F + kDpCols - 1) / kDpCols;
+  const int64_t blocks = (int64_t)((T + rows - 1) / rows) * col_blocks + un.blocks;
   const uint16_t *p = static_cast<const uint16_t*>(P), *y = static_cast<const uint16_t*>(dY);
   uint16_t* o = static_cast<uint16_t*>(dp);
   auto kern = vec ? (part ? gated_dp_kernel<DT, true, true> : gated_dp_kernel<DT, true, false>)
                   : (part ? gated_dp_kernel<DT, false, true> : gated_dp_kernel<DT, false, false>);
-  return launch_pdl(kern, grid, 32 * kDpWarps, 0, s, 0, p, y, T, F, pitch, act, o, part);
+  return launch_pdl(kern, dim3((unsigned)blocks), 32 * kDpWarps, 0, s, 0, p, y, T, F, pitch, act, o, part, rows, col_blocks,
+                    un);
 }
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -489,9 +534,51 @@ struct GradWs {
     dp = 0;
     wm = dp + align256(T * 2 * pitch * 2);
     part = wm + align256(h->n_out * h->k * 2);
-    total = part + align256((T + kDpRows - 1) / kDpRows * h->n_out * 4);
+    const int64_t rows = dp_block_rows(T, F);
+    total = part + align256((T + rows - 1) / rows * h->n_out * 4);
   }
 };
+
+// Tiles of both products for tiles bn columns wide, shared out over at most
+// `pairs` CTA pairs: side 0 (the longer sums) goes round the pairs, side 1 goes on
+// top so that the fullest pair has the least to do.  Returns that pair's stages
+// (with a fixed part per tile), -1 when there are too many tiles.
+int64_t plan_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw, int bn, int pairs, GradArgs* a, int* grid) {
+  constexpr int kFixed = 6;  // a tile's fill and drain, in stages
+  const int64_t F = h->n_out / 2;
+  const int n_nt = (int)((h->k + bn - 1) / bn);
+  a->F = (int)F;
+  a->T = (int)T;
+  a->k = (int)h->k;
+  a->kb_half = (int)((F + kGradKb - 1) / kGradKb);
+  GradSide sw{}, sx{};
+  sw.dw = 1;
+  sw.n_nt = sx.n_nt = n_nt;
+  sw.n_mt = (int)((F + 255) / 256);
+  sw.n_kb = (int)((T + kGradKb - 1) / kGradKb);
+  sx.n_mt = (int)((T + 255) / 256);
+  sx.n_kb = 2 * a->kb_half;
+  const int64_t w_tiles = want_dw ? 2 * (int64_t)sw.n_mt * n_nt : 0, x_tiles = want_dx ? (int64_t)sx.n_mt * n_nt : 0;
+  if (w_tiles > INT32_MAX / 2 || x_tiles > INT32_MAX / 2) return -1;
+  sw.tiles = (int)w_tiles;
+  sx.tiles = (int)x_tiles;
+  const bool w_first = sw.n_kb >= sx.n_kb;
+  a->side[0] = w_first ? sw : sx;
+  a->side[1] = w_first ? sx : sw;
+  *grid = (int)std::min<int64_t>(w_tiles + x_tiles, pairs);
+  const int64_t c0 = a->side[0].n_kb + kFixed, c1 = a->side[1].n_kb + kFixed;
+  const int64_t q = a->side[0].tiles / *grid;
+  a->hi = a->side[0].tiles % *grid;
+  int64_t lo = 0, hi = 0;
+  for (int64_t level = (a->side[1].tiles * c1 + a->side[0].tiles * c0) / *grid;; level += c1 / 8 + 1) {
+    lo = std::max<int64_t>(0, (level - q * c0) / c1);
+    hi = a->hi ? std::max<int64_t>(0, (level - (q + 1) * c0) / c1) : lo;
+    if (lo * (*grid - a->hi) + hi * a->hi >= a->side[1].tiles) break;
+  }
+  a->lo_tiles = (int)lo;
+  a->hi_tiles = (int)hi;
+  return std::max(q * c0 + lo * c1, a->hi ? (q + 1) * c0 + hi * c1 : 0);
+}
 
 nm_status check_grad(const nm_handle* h, int64_t T) {
   nm_status st = check_handle(h);
@@ -566,60 +653,59 @@ nm_status nm_gated_backward(const nm_handle* h, const void* X, const void* P, co
   uint8_t* base = static_cast<uint8_t*>(ws);
   void* dp = base + lay.dp;
   float* part = dbias ? reinterpret_cast<float*>(base + lay.part) : nullptr;
-  const int row_blocks = (int)((T + kDpRows - 1) / kDpRows);
-  if (row_blocks > 65535) return fail(NM_ERR_UNSUPPORTED, "T above %d", 65535 * kDpRows);
-
+  const int rows = dp_block_rows(T, F), row_blocks = (int)((T + rows - 1) / rows);
+  UnpackArgs un{};
+  if (dX) {
+    un.bpack = h->d_bpack;
+    un.Wm = reinterpret_cast<uint16_t*>(base + lay.wm);
+    un.K = h->k;
+    un.units = h->n_out * ((h->k + 15) / 16);
+    un.img = h->img;
+    un.n_kb = h->n_kb;
+    un.n_ff = (int)F;
+    un.blocks = (int)((un.units + 32 * kDpWarps - 1) / (32 * kDpWarps));
+  }
+  if ((int64_t)row_blocks * ((F + kDpCols - 1) / kDpCols) + un.blocks > INT32_MAX)
+    return fail(NM_ERR_UNSUPPORTED, "T x n_ff too large");
   cudaError_t e = cudaSuccess;
-  if (dX && (e = launch_decompress(h, base + lay.wm, s)) != cudaSuccess) return cuda_fail(e, "unpack the weight");
   const bool vec = F % 8 == 0;  // every row starts on 16 bytes
-  e = h->dt == DT_F16 ? launch_dp<DT_F16>(vec, P, dY, (int)T, (int)F, (int)lay.pitch, (int)act, dp, part, s)
-                      : launch_dp<DT_BF16>(vec, P, dY, (int)T, (int)F, (int)lay.pitch, (int)act, dp, part, s);
+  e = h->dt == DT_F16 ? launch_dp<DT_F16>(vec, P, dY, (int)T, (int)F, (int)lay.pitch, (int)act, dp, part, un, s)
+                      : launch_dp<DT_BF16>(vec, P, dY, (int)T, (int)F, (int)lay.pitch, (int)act, dp, part, un, s);
   if (e != cudaSuccess) return cuda_fail(e, "launch the gradient of the output stage");
 
   if (dX || dW) {
     const int pairs = num_sms(h->device) / 2;
-    const int bn = h->k > 128 ? 256 : 128;
-    const int n_nt = (int)((h->k + bn - 1) / bn);
+    // Tile width: the lower estimate of the fullest pair's work.  A stage of a
+    // 256-wide tile takes 1.45 times a 128-wide one's (0.33 against 0.23 us over
+    // full waves, 0.28 against 0.19 when few tiles run; the narrower tile moves
+    // 24 KB a stage and SM against 32 KB for half the products).
     GradArgs a{};
-    a.F = (int)F;
-    a.T = (int)T;
-    a.k = (int)h->k;
+    int bn = 0, grid = 0;
+    double best = 1e300;
+    const char* forced = getenv("NMSPMM_FORCE_GRAD_BN");  // tests and sweeps
+    const int forced_bn = forced && *forced ? atoi(forced) : 0;
+    for (int w : {256, 128}) {
+      if (forced_bn && w != forced_bn) continue;
+      GradArgs c{};
+      int g = 0;
+      const int64_t level = plan_grad(h, T, dX != nullptr, dW != nullptr, w, pairs, &c, &g);
+      if (level < 0) return fail(NM_ERR_UNSUPPORTED, "T x k too large");
+      const double cost = (double)level * (w == 256 ? 1.45 : 1.0);
+      if (cost < best) {
+        best = cost;
+        a = c;
+        bn = w;
+        grid = g;
+      }
+    }
+    if (!bn) return fail(NM_ERR_INVALID, "NMSPMM_FORCE_GRAD_BN must be 128 or 256");
     a.dW = dW;
     a.dX = dX;
+    a.part = part;
+    a.dbias = dbias;
+    a.row_blocks = row_blocks;
     a.err = h->d_err;
     a.timeout_ns = 1000000000ull;
-    a.kb_half = (int)((F + kGradKb - 1) / kGradKb);
-    GradSide sw{}, sx{};
-    sw.dw = 1;
-    sw.n_nt = n_nt;
-    sw.n_mt = (int)((F + 255) / 256);
-    sw.n_kb = (int)((T + kGradKb - 1) / kGradKb);
-    sw.tiles = dW ? 2 * sw.n_mt * n_nt : 0;
-    sx.n_nt = n_nt;
-    sx.n_mt = (int)((T + 255) / 256);
-    sx.n_kb = 2 * a.kb_half;
-    const int64_t x_tiles = dX ? (int64_t)sx.n_mt * n_nt : 0;
-    if (x_tiles > INT32_MAX / 2) return fail(NM_ERR_UNSUPPORTED, "T x k too large");
-    sx.tiles = (int)x_tiles;
-    const bool w_first = sw.n_kb >= sx.n_kb;
-    a.side[0] = w_first ? sw : sx;
-    a.side[1] = w_first ? sx : sw;
-    const int64_t total = (int64_t)sw.tiles + sx.tiles;
-    const int grid = (int)std::min<int64_t>(total, pairs);
-    // Share out side 1 on top of side 0 so that the fullest pair has the least to
-    // do: the lowest level L (in stages) at which every tile finds room.
-    const int kFixed = 6;  // a tile's fill and drain, in stages
-    const int64_t c0 = a.side[0].n_kb + kFixed, c1 = a.side[1].n_kb + kFixed;
-    const int64_t q = a.side[0].tiles / grid;
-    a.hi = a.side[0].tiles % grid;
-    int64_t lo = 0, hi = 0;
-    for (int64_t need = (a.side[1].tiles * c1 + a.side[0].tiles * c0) / grid;; need += c1 / 8 + 1) {
-      lo = std::max<int64_t>(0, (need - q * c0) / c1);
-      hi = a.hi ? std::max<int64_t>(0, (need - (q + 1) * c0) / c1) : lo;
-      if (lo * (grid - a.hi) + hi * a.hi >= a.side[1].tiles) break;
-    }
-    a.lo_tiles = (int)lo;
-    a.hi_tiles = (int)hi;
 
     GradMaps m;
     const int dt = h->dt;
@@ -636,9 +722,9 @@ nm_status nm_gated_backward(const nm_handle* h, const void* X, const void* P, co
                                   : launch_grad_t<DT_BF16, 128>(grid, m, a, s));
     if (e != cudaSuccess) return cuda_fail(e, "launch the gradient products");
   }
-  if (dbias) {
-    e = launch_pdl(dbias_kernel, dim3((unsigned)((h->n_out + 31) / 32)), 256, 0, s, 0, (const float*)part, (int)h->n_out,
-                   row_blocks, dbias);
+  if (dbias && !dX && !dW) {
+    e = launch_pdl(dbias_kernel, dim3((unsigned)((h->n_out + 127) / 128)), 128, 0, s, 0, (const float*)part,
+                   (int)h->n_out, row_blocks, dbias);
     if (e != cudaSuccess) return cuda_fail(e, "launch the bias gradient");
   }
   return NM_OK;

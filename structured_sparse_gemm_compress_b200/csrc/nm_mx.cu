@@ -727,6 +727,7 @@ nm_status mx_product(const nm_handle* h, const void* Q, const void* S, int64_t T
       slot = i;
     }
   }
+  if (best == 1e300) return fail(NM_ERR_INVALID, "NMSPMM_FORCE_MX_BN must be 64, 128 or 192");
   const int bn = kMxTiles[slot];
   a.n_nt = (int)((h->mx_rows + bn - 1) / bn);
   const int64_t units = n_mt * a.n_nt;

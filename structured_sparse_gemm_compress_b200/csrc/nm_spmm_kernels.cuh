@@ -57,6 +57,9 @@ constexpr int kOutEpi = 8;
 // channels beside their 16 up channels, so one warp's 32 lanes hold both halves
 // of 16 output channels.
 constexpr int kOutGate = 16;
+// bit 5 = two-SM kernel with the gated output stage: p goes out through shared
+// memory in whole 128-byte runs (16-bit handles, n_ff a multiple of 8).
+constexpr int kOutSave = 32;
 constexpr int out_bytes(int out) { return ((out & 3) == OUT_I32 || (out & 3) == OUT_F32) ? 4 : 2; }
 // Epilogue warps and CTA size of a kernel with output code OUT.
 constexpr int epi_warps(int out) { return 4 * epw_for((out & kOutEpi) != 0); }
@@ -404,9 +407,15 @@ __device__ __forceinline__ void gate_store(const SpmmArgs& a, const float (&y)[H
 }
 
 // One warp's run of CH tokens starting at token t0; row: this lane's packed row.
-template <int DT, int CH>
+// STAGED: p leaves by way of pbuf (kOutSave), shared by the four warps `part` of
+// the tile's lane quarters: [CH tokens][gate, up][64 channels], the 16-byte pieces
+// of the up half rotated by 64 bytes so that a warp's gate and up lanes write
+// different banks.  Directly, each of a warp's stores of p covers two 32-byte
+// runs, and saving p took 30 us of an 87 us launch (6304 x 1024 -> 2 x 4096);
+// gathered, a store covers four whole lines.
+template <int DT, int CH, bool STAGED = false>
 __device__ __forceinline__ void gate_run(const SpmmArgs& a, const EpiCh& e, const uint32_t (&r)[CH], int row, int t0,
-                                         int lane) {
+                                         int lane, uint8_t* pbuf = nullptr, int part = 0) {
   constexpr int H = CH / 2;
   float f[CH];
 #pragma unroll
@@ -423,16 +432,21 @@ __device__ __forceinline__ void gate_run(const SpmmArgs& a, const EpiCh& e, cons
   }
   const int ch = (row >> 5) * 16 + (row & 15);
   const bool ch_ok = ch < a.n_ff;
-  if constexpr (DT != DT_I8) {
+  const bool up = (lane & 16) != 0;
+  if constexpr (STAGED) {
+    const uint32_t c = (uint32_t)(ch & 63) * 2u;  // byte of the channel within the tile's half row
+    uint8_t* dst = pbuf + (up ? 128u : 0u) + (c ^ (up ? 64u : 0u));
+#pragma unroll
+    for (int j = 0; j < CH; ++j) gate_save<DT>(dst + j * 256, 0, f[j]);
+  } else if constexpr (DT != DT_I8) {
     if (a.P && ch_ok) {
-      const size_t base = (size_t)t0 * (2 * (size_t)a.n_ff) + (size_t)((row & 16) ? a.n_ff + ch : ch);
+      const size_t base = (size_t)t0 * (2 * (size_t)a.n_ff) + (size_t)(up ? a.n_ff + ch : ch);
 #pragma unroll
       for (int j = 0; j < CH; ++j)
         if (t0 + j < a.T) gate_save<DT>(a.P, base + (size_t)j * (2 * (size_t)a.n_ff), f[j]);
     }
   }
   __syncwarp();
-  const bool up = (lane & 16) != 0;
   float g[H], u[H];
 #pragma unroll
   for (int j = 0; j < H; ++j) {
@@ -443,14 +457,28 @@ __device__ __forceinline__ void gate_run(const SpmmArgs& a, const EpiCh& e, cons
   act_run<H>(g, a.act);
 #pragma unroll
   for (int j = 0; j < H; ++j) g[j] = __fmul_rn(g[j], u[j]);
-  if (!ch_ok) return;
-  const int ty = up ? t0 + H : t0;
-  const size_t base = (size_t)ty * a.n_ff + ch;
-  switch (a.out_ty) {
-    case OUT_F16: gate_store<OUT_F16, H>(a, g, base, a.T - ty); break;
-    case OUT_BF16: gate_store<OUT_BF16, H>(a, g, base, a.T - ty); break;
-    case OUT_I8: gate_store<OUT_I8, H>(a, g, base, a.T - ty); break;
-    default: gate_store<OUT_F32, H>(a, g, base, a.T - ty); break;
+  if (ch_ok) {
+    const int ty = up ? t0 + H : t0;
+    const size_t base = (size_t)ty * a.n_ff + ch;
+    switch (a.out_ty) {
+      case OUT_F16: gate_store<OUT_F16, H>(a, g, base, a.T - ty); break;
+      case OUT_BF16: gate_store<OUT_BF16, H>(a, g, base, a.T - ty); break;
+      case OUT_I8: gate_store<OUT_I8, H>(a, g, base, a.T - ty); break;
+      default: gate_store<OUT_F32, H>(a, g, base, a.T - ty); break;
+    }
+  }
+  if constexpr (STAGED) {
+    named_bar_sync(1 + part, 128);  // all four lane quarters' p of these tokens are in pbuf
+    const int tid = ((row >> 5) & 3) * 32 + lane, ch0 = (row >> 7) * 64;
+#pragma unroll
+    for (int i = 0; i < CH / 8; ++i) {
+      const int piece = tid + 128 * i, t = t0 + piece / 16, z = (piece >> 3) & 1, c = piece & 7;
+      if (t < a.T && ch0 + c * 8 < a.n_ff) {
+        const uint4 q = *reinterpret_cast<const uint4*>(pbuf + (piece / 16) * 256 + z * 128 + ((c * 16) ^ (z * 64)));
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.P) + (size_t)t * (2 * (size_t)a.n_ff) +
+                                  (size_t)z * a.n_ff + ch0 + c * 8) = q;
+      }
+    }
   }
 }
 
@@ -1253,7 +1281,9 @@ struct PairCfg {
   static constexpr int OES = out_bytes(OUT);
   static constexpr int EPI_BUF = CH * 32 * OES;
   static constexpr int EPI_NB = (kSmemBudget - 2 * EPI_WARPS * EPI_BUF) / STAGE >= 4 ? 2 : 1;
-  static constexpr int EPI_BYTES = TS ? EPI_NB * EPI_WARPS * EPI_BUF : 0;
+  // kOutSave: two buffers of CH tokens x 128 packed rows for each group of four warps
+  static constexpr int SAVE_BUF = CH * 256;
+  static constexpr int EPI_BYTES = TS ? EPI_NB * EPI_WARPS * EPI_BUF : (OUT & kOutSave) ? EPI_WARPS / 4 * 2 * SAVE_BUF : 0;
   static constexpr int STAGES_FIT = (kSmemBudget - EPI_BYTES) / STAGE;
   static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
   static constexpr int SMEM = STAGES * STAGE + EPI_BYTES + 1024;
@@ -1274,6 +1304,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(cta_threads(OUT), 1)
   constexpr bool GATE = (OUT & kOutGate) != 0;
   static_assert(!EPI || !C::TS, "the runtime output stage stores directly");
   static_assert(!GATE || EPI, "the gated output stage is a runtime one");
+  constexpr bool SAVE = (OUT & kOutSave) != 0;
+  static_assert(!SAVE || (GATE && DT != DT_I8), "p is saved by 16-bit gated kernels");
   constexpr int KIND = DT == DT_I8 ? 0 : 1;
 
   extern __shared__ uint8_t smem_raw[];
@@ -1286,6 +1318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(cta_threads(OUT), 1)
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_sh;
+  __shared__ volatile int part_ok_sh[SAVE ? C::EPI_WARPS / 4 : 1][2];
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -1497,14 +1530,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(cta_threads(OUT), 1)
     const int part = ew >> 2;
     uint8_t* stage_buf = smem + (size_t)C::STAGES * C::STAGE + (size_t)ew * C::EPI_NB * C::EPI_BUF;
     int buf = 0, acc = 0, iter = 0;
+    [[maybe_unused]] int pchunk = 0;  // kOutSave: chunks staged so far
     uint32_t acc_phase = 0;
     for (int u = u_first; u < a.units; u += u_step, ++iter) {
       const int pt = u % n_pct, tt = u / n_pct;
       const int ct = 2 * pt + (int)rank;
-      // No named barrier in this loop: each warp waits for the accumulator itself.
-      if (!mbar_wait_warp(&accf_bar[acc], acc_phase, &abort_sh, tmo)) {
-        if (lane == 0) give_up(4);
-        break;
+      if constexpr (SAVE) {
+        // The four warps of a part meet at named barriers below: one of them waits
+        // and all take the same branch (the flag alternates between two slots).
+        if ((ew & 3) == 0) {
+          const bool got = mbar_wait_warp(&accf_bar[acc], acc_phase, &abort_sh, tmo);
+          if (lane == 0) {
+            if (!got) give_up(4);
+            part_ok_sh[part][iter & 1] = got ? 1 : 0;
+          }
+        }
+        named_bar_sync(1 + part, 128);
+        if (!part_ok_sh[part][iter & 1]) break;
+      } else {
+        // No named barrier in this loop: each warp waits for the accumulator itself.
+        if (!mbar_wait_warp(&accf_bar[acc], acc_phase, &abort_sh, tmo)) {
+          if (lane == 0) give_up(4);
+          break;
+        }
       }
       if (ep_tid == 0) NM_TR(TR_E_START, iter);
       tc_fence_after();
@@ -1554,7 +1602,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(cta_threads(OUT), 1)
           }
           if (C::EPI_NB == 2) buf ^= 1;
         } else if constexpr (GATE) {
-          gate_run<DT, C::CH>(a, EpiCh{s, bch}, r, ch, tc0, lane);
+          if constexpr (SAVE) {
+            uint8_t* pbuf = smem + (size_t)C::STAGES * C::STAGE + (size_t)(2 * part + (pchunk & 1)) * C::SAVE_BUF;
+            gate_run<DT, C::CH, true>(a, EpiCh{s, bch}, r, ch, tc0, lane, pbuf, part);
+            ++pchunk;
+          } else {
+            gate_run<DT, C::CH>(a, EpiCh{s, bch}, r, ch, tc0, lane);
+          }
         } else if (ch_ok) {
           if constexpr (EPI) {
             epi_run<DT, C::CH>(a, EpiCh{s, bch}, r, (size_t)tc0 * a.n_out + ch, a.T - tc0);

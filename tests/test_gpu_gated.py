@@ -39,7 +39,7 @@ ACTS = ["none", "gelu", "silu", "relu"]
 @pytest.fixture(autouse=True)
 def _no_forced_plan(monkeypatch):
     for k in ("NMSPMM_FORCE_BN", "NMSPMM_FORCE_SPLITK", "NMSPMM_FORCE_XS", "NMSPMM_FORCE_GRID",
-              "NMSPMM_FORCE_PAIR", "NMSPMM_SPLIT_GLOBAL"):
+              "NMSPMM_FORCE_PAIR", "NMSPMM_SPLIT_GLOBAL", "NMSPMM_FORCE_GRAD_BN"):
         monkeypatch.delenv(k, raising=False)
 
 
@@ -138,11 +138,12 @@ def test_forward_output_stage(dt, out, act):
 
 
 @pytest.mark.parametrize("dt,image", [("int8", (2, 4)), ("int8", (4, 8)), ("bf16", (2, 4)), ("fp16", (4, 4))])
-@pytest.mark.parametrize("pair,bn", [(0, 32), (0, 64), (0, 128), (0, 192), (1, 128), (1, 192), (1, 224)])
-def test_forced_tiles(monkeypatch, dt, image, pair, bn):
+@pytest.mark.parametrize("pair,bn", [(0, 32), (0, 64), (0, 128), (0, 192), (1, 128), (1, 192)])
+@pytest.mark.parametrize("F", [147, 152])       # p stored element by element, in whole runs
+def test_forced_tiles(monkeypatch, dt, image, pair, bn, F):
     monkeypatch.setenv("NMSPMM_FORCE_PAIR", str(pair))
     monkeypatch.setenv("NMSPMM_FORCE_BN", str(bn))
-    h, _ = check_forward(dt, 461, 320, 147, *image, save=dt != "int8", out="float16")
+    h, _ = check_forward(dt, 461, 320, F, *image, save=dt != "int8", out="float16")
     plan = nm.nm_plan_query(h, 461)
     if not (bn == 192 and pair == 0 and image != (2, 4)):   # two stages only: the planner keeps to 128
         assert (plan["pair"], plan["bn"]) == (pair, bn)
@@ -268,9 +269,11 @@ def test_backward_activations_and_patterns(dt, act, N, M):
     check_backward(dt, 150, 192, 72, N, M, act=act, seed=3)
 
 
-@pytest.mark.parametrize("T,k,F", [(2500, 768, 700), (300, 1024, 2600)])
-def test_backward_many_tiles(T, k, F):
-    """More tiles than CTA pairs, each product in turn the one with the longer sums."""
+@pytest.mark.parametrize("bn", [128, 256])
+@pytest.mark.parametrize("T,k,F", [(2500, 768, 700), (300, 1024, 2600), (130, 200, 96)])
+def test_backward_many_tiles(monkeypatch, T, k, F, bn):
+    """More tiles than CTA pairs, each product in turn the one with the longer sums; both tile widths."""
+    monkeypatch.setenv("NMSPMM_FORCE_GRAD_BN", str(bn))
     check_backward("bf16", T, k, F, act="gelu", seed=1)
 
 

@@ -212,6 +212,16 @@ def test_product_sizes(T, k, n):
     run_product(T, k, n, seed=T + n)
 
 
+@pytest.mark.parametrize("bn", [64, 128, 192])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("out", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n", [512, 514, 1030])
+def test_every_tile_width(monkeypatch, n, out, gated, bn):
+    """Tiles that start anywhere in a scale tile; several tiles per CTA pair in the last case."""
+    monkeypatch.setenv("NMSPMM_FORCE_MX_BN", str(bn))
+    run_product(300, 288, n, out=out, act="gelu", bias=True, gated=gated, seed=n)
+
+
 @pytest.mark.parametrize("out", ["float32", "float16", "bfloat16", "default"])
 @pytest.mark.parametrize("scale,bias,act", [(False, False, "none"), (True, False, "gelu"), (False, True, "none"),
                                             (True, True, "gelu")])
