@@ -142,6 +142,10 @@ def _check_tensor(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) 
         raise ValueError(f"{name} must be on the current CUDA device")
 
 
+def _library() -> ctypes.CDLL:
+    return _lib if _lib is not None else lib()
+
+
 class NMHandle:
     """One compressed weight (owns the library handle and its device memory)."""
 
@@ -366,7 +370,9 @@ def nm_spmm_gated(h: NMHandle, X: torch.Tensor, Y: torch.Tensor | None = None, P
         _check_tensor("Y", Y, want, (T, n))
     if P is not None:
         _check_tensor("P", P, h.dtype, (T, h.n_out))
-    _check(lib().nm_spmm_gated(h.raw, X.data_ptr(), T, Y.data_ptr(), _ptr(P), ctypes.byref(ep), _stream(stream)))
+    status = _library().nm_spmm_gated(h.raw, X.data_ptr(), T, Y.data_ptr(), _ptr(P), ep, _stream(stream))
+    if status:
+        _check(status)
     return Y
 
 
@@ -423,11 +429,15 @@ def nm_mx_quantize(X: torch.Tensor, Q: torch.Tensor | None = None, S: torch.Tens
                    stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """X [T, k] (fp32 / fp16 / bf16, rows contiguous, any row stride that is a
     multiple of 16 bytes) to microscaled 4-bit codes Q [T, k / 2] and scales S (uint8)."""
-    if X.dim() != 2 or X.dtype not in _MX_DT or (X.shape[1] > 1 and X.stride(1) != 1):
+    dt = _MX_DT.get(X.dtype)
+    if dt is None or X.dim() != 2:
+        raise ValueError("X must be a [T, k] float32/float16/bfloat16 tensor with contiguous rows")
+    T, k = X.shape
+    ldx, step = X.stride()
+    if step != 1 and k > 1:
         raise ValueError("X must be a [T, k] float32/float16/bfloat16 tensor with contiguous rows")
     if not X.is_cuda or X.get_device() != _current_device():
         raise ValueError("X must be on the current CUDA device")
-    T, k = X.shape
     n = (T + 127) // 128 * ((k + 255) // 256) * 1024
     if Q is None:
         Q = _empty((T, k // 2), torch.uint8, X.device, stream)
@@ -437,17 +447,19 @@ def nm_mx_quantize(X: torch.Tensor, Q: torch.Tensor | None = None, S: torch.Tens
         S = _empty((n,), torch.uint8, X.device, stream)
     else:
         _check_tensor("S", S, torch.uint8, (n,))
-    ldx = X.stride(0) if T > 1 else k
-    _check(lib().nm_mx_quantize(X.data_ptr(), T, k, ldx, _MX_DT[X.dtype], Q.data_ptr(), S.data_ptr(),
-                                _stream(stream)))
+    status = _library().nm_mx_quantize(X.data_ptr(), T, k, ldx if T > 1 else k, dt, Q.data_ptr(), S.data_ptr(),
+                                       _stream(stream))
+    if status:
+        _check(status)
     return Q, S
 
 
 def _check_mx(Q: torch.Tensor, S: torch.Tensor) -> tuple[int, int]:
     if Q.dim() != 2:
         raise ValueError("Q must be [T, k / 2]")
-    T, k = Q.shape[0], 2 * Q.shape[1]
-    _check_tensor("Q", Q, torch.uint8, (T, k // 2))
+    T, half = Q.shape
+    k = 2 * half
+    _check_tensor("Q", Q, torch.uint8, (T, half))
     _check_tensor("S", S, torch.uint8, ((T + 127) // 128 * ((k + 255) // 256) * 1024,))
     return T, k
 
@@ -462,7 +474,9 @@ def nm_mx_dequantize(Q: torch.Tensor, S: torch.Tensor, dtype: torch.dtype = torc
         X = _empty((T, k), dtype, Q.device, stream)
     else:
         _check_tensor("X", X, dtype, (T, k))
-    _check(lib().nm_mx_dequantize(Q.data_ptr(), S.data_ptr(), T, k, _MX_DT[dtype], X.data_ptr(), _stream(stream)))
+    status = _library().nm_mx_dequantize(Q.data_ptr(), S.data_ptr(), T, k, _MX_DT[dtype], X.data_ptr(), _stream(stream))
+    if status:
+        _check(status)
     return X
 
 
@@ -491,8 +505,9 @@ def _mx_product(name: str, h: NMHandle, Q, S, Y, scale, bias, act: str, out: str
         Y = _empty((T, n), want, Q.device, stream)
     else:
         _check_tensor("Y", Y, want, (T, n))
-    _check(getattr(lib(), name)(h.raw, Q.data_ptr(), S.data_ptr(), T, Y.data_ptr(), ctypes.byref(ep),
-                                _stream(stream)))
+    status = getattr(_library(), name)(h.raw, Q.data_ptr(), S.data_ptr(), T, Y.data_ptr(), ep, _stream(stream))
+    if status:
+        _check(status)
     return Y
 
 

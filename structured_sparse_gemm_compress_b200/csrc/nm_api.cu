@@ -16,6 +16,8 @@
 #include <new>
 #include <string>
 
+#include <unistd.h>
+
 #include "nmspmm.h"
 #include "nm_device.cuh"
 #include "nm_internal.h"
@@ -78,7 +80,21 @@ using nm::EpiReq;
 using nm::fail;
 using nm::num_sms;
 
+// The overrides are read at every call (tests change them between calls); a
+// call looks ten of them up, so one pass over the environment says first whether
+// there are any (plan_with, the first step of every call that reads them).
+thread_local bool g_env_any = true;
+void scan_env() {
+  g_env_any = false;
+  for (char** e = environ; e && *e; ++e)
+    if ((*e)[0] == 'N' && strncmp(*e, "NMSPMM_", 7) == 0) {
+      g_env_any = true;
+      return;
+    }
+}
+
 int env_int(const char* name, int dflt) {
+  if (!g_env_any) return dflt;
   const char* v = getenv(name);
   return (v && *v) ? atoi(v) : dflt;
 }
@@ -339,6 +355,7 @@ void choose_cluster_split(const nm_handle* h, int64_t T, int sms, int forced_bn,
 // given the resident-cluster capacities.
 nm::Plan plan_with(const nm_handle* h, int64_t T, int sms, const Capacity& capacity) {
   nm::Plan p;
+  scan_env();
   const int forced_bn = env_int("NMSPMM_FORCE_BN", 0);
   const int forced_split = env_int("NMSPMM_FORCE_SPLITK", 0);
   const int forced_xs = env_int("NMSPMM_FORCE_XS", -1);  // -1 auto, 0 off, 1 on when eligible

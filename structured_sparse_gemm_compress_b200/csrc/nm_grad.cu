@@ -530,7 +530,7 @@ struct GradWs {
   int64_t pitch, dp, wm, part, total;
   GradWs(const nm_handle* h, int64_t T) {
     const int64_t F = h->n_out / 2;
-    pitch = (F + 7) / 8 * 8;
+    pitch = (F + 63) / 64 * 64;  // whole 128-byte lines: a 128-byte box row then touches one
     dp = 0;
     wm = dp + align256(T * 2 * pitch * 2);
     part = wm + align256(h->n_out * h->k * 2);
