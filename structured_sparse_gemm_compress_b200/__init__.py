@@ -1,6 +1,7 @@
 """B200-native N:M semi-structured sparse weight x dense activation GEMM.
 
-A thin ctypes binding over ``libnmspmm.so`` (C ABI in ``include/nmspmm.h``).
+A thin binding over ``libnmspmm.so`` (C ABI in ``include/nmspmm.h``): ctypes, and a
+small compiled module for the calls that are made on few tokens.
 Every step of the path runs in the library's sm_100a kernels; this module only
 marshals torch tensors (device memory and streams) into the C calls, with the
 same names.  There is no fallback: if the library is missing or a call fails,
@@ -124,16 +125,6 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """An output that belongs to the stream the call runs on (torch's allocator
-    then never hands its memory to work that is not ordered behind it)."""
-    if stream is None:  # (empty_strided: two thirds of torch.empty's time per call)
-        return torch.empty_strided(shape, (1,) if len(shape) == 1 else (shape[1], 1), dtype=dtype, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(s):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
 def _check_tensor(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) -> None:
     """A contiguous tensor of this type and shape on the current CUDA device."""
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
@@ -142,8 +133,26 @@ def _check_tensor(name: str, t: torch.Tensor, dtype: torch.dtype, shape: tuple) 
         raise ValueError(f"{name} must be on the current CUDA device")
 
 
-def _library() -> ctypes.CDLL:
-    return _lib if _lib is not None else lib()
+_module = None
+
+
+def _native():
+    """The compiled binding (csrc/nm_binding.cpp) of the feed-forward and microscaled
+    calls, which spend a quarter of ctypes' time on the host; speaks to the same
+    library as ``lib()``."""
+    global _module
+    if _module is None:
+        L = lib()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError(f"the compiled binding is missing or does not load ({e}): build it with "
+                               "`python -m structured_sparse_gemm_compress_b200.build`") from e
+        _binding.init(_check, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+            "nm_mx_quantize", "nm_mx_dequantize", "nm_spmm_mx", "nm_spmm_mx_gated", "nm_spmm_gated",
+            "nm_gated_backward", "nm_gated_backward_workspace")))
+        _module = _binding
+    return _module
 
 
 class NMHandle:
@@ -328,15 +337,10 @@ def nm_spmm_gather_ex(h: NMHandle, Xt: torch.Tensor, T: int | None = None, Y: to
     return Y
 
 
-def _epilogue(h: NMHandle, scale, bias, act: str, out: str, out_scale: float) -> NMEpilogue:
-    """``nm_epilogue`` of a call on ``h`` after checking what the C side cannot see."""
+def _codes(act: str, out: str) -> tuple[int, int]:
     if out not in OUT_TYPES or act not in ACTS:
         raise ValueError(f"out must be one of {tuple(OUT_TYPES)}, act one of {tuple(ACTS)}")
-    if scale is not None:
-        _check_tensor("scale", scale, torch.float32, (h.n_out,))
-    if bias is not None:
-        _check_tensor("bias", bias, torch.float32, (h.n_out,))
-    return NMEpilogue(OUT_TYPES[out], ACTS[act], _ptr(scale), _ptr(bias), float(out_scale))
+    return ACTS[act], OUT_TYPES[out]
 
 
 def nm_compress_gated(W: torch.Tensor, N: int, M: int, stream=None) -> NMHandle:
@@ -358,22 +362,9 @@ def nm_spmm_gated(h: NMHandle, X: torch.Tensor, Y: torch.Tensor | None = None, P
     """Y [T, n_ff] = act(g) * u with g, u the halves of X @ Wm^T * scale + bias, in
     one kernel.  P [T, 2 n_ff] (the handle's type), if given, receives g and u for
     ``nm_gated_backward``."""
-    if X.dim() != 2:
-        raise ValueError("X must be [T, k]")
-    T, n = X.shape[0], h.n_out // 2
-    _check_tensor("X", X, h.dtype, (T, h.k))
-    ep = _epilogue(h, scale, bias, act, out, out_scale)
-    want = (torch.float32 if h.dt == NM_INT8 else h.dtype) if out == "default" else _OUT_TORCH[out]
-    if Y is None:
-        Y = _empty((T, n), want, X.device, stream)
-    else:
-        _check_tensor("Y", Y, want, (T, n))
-    if P is not None:
-        _check_tensor("P", P, h.dtype, (T, h.n_out))
-    status = _library().nm_spmm_gated(h.raw, X.data_ptr(), T, Y.data_ptr(), _ptr(P), ep, _stream(stream))
-    if status:
-        _check(status)
-    return Y
+    act_code, out_code = _codes(act, out)
+    return (_module or _native()).spmm_gated(h.raw.value, h.n_out, h.k, h.dt, X, Y, P, scale, bias, act_code, out_code,
+                                             out_scale, stream)
 
 
 def nm_gated_backward_workspace(h: NMHandle, T: int) -> int:
@@ -389,33 +380,10 @@ def nm_gated_backward(h: NMHandle, X: torch.Tensor, P: torch.Tensor, dY: torch.T
     """Gradients of ``nm_spmm_gated`` (fp16 / bf16 handles): (dX [T, k], dW [2 n_ff,
     k], dbias [2 n_ff] fp32 or None).  dW is the gradient of the masked weight at
     every position.  ``workspace``: a uint8 CUDA tensor, else one is allocated."""
-    if X.dim() != 2 or act not in ACTS:
-        raise ValueError(f"X must be [T, k], act one of {tuple(ACTS)}")
-    T, n = X.shape[0], h.n_out // 2
-    dt = h.dtype
-    _check_tensor("X", X, dt, (T, h.k))
-    _check_tensor("P", P, dt, (T, h.n_out))
-    _check_tensor("dY", dY, dt, (T, n))
-    if dX is None:
-        dX = _empty((T, h.k), dt, X.device, stream)
-    else:
-        _check_tensor("dX", dX, dt, (T, h.k))
-    if dW is None:
-        dW = _empty((h.n_out, h.k), dt, X.device, stream)
-    else:
-        _check_tensor("dW", dW, dt, (h.n_out, h.k))
-    if dbias is not None:
-        _check_tensor("dbias", dbias, torch.float32, (h.n_out,))
-    elif bias_grad:
-        dbias = _empty((h.n_out,), torch.float32, X.device, stream)
-    if workspace is None:
-        workspace = _empty((nm_gated_backward_workspace(h, T),), torch.uint8, X.device, stream)
-    else:
-        _check_tensor("workspace", workspace, torch.uint8, (workspace.numel(),))
-    _check(lib().nm_gated_backward(h.raw, X.data_ptr(), P.data_ptr(), dY.data_ptr(), T, ACTS[act], dX.data_ptr(),
-                                   dW.data_ptr(), _ptr(dbias), workspace.data_ptr(), workspace.numel(),
-                                   _stream(stream)))
-    return dX, dW, dbias
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {tuple(ACTS)}")
+    return (_module or _native()).gated_backward(h.raw.value, h.n_out, h.k, h.dt, X, P, dY, ACTS[act], int(bias_grad), dX,
+                                                 dW, dbias, workspace, stream)
 
 
 def nm_mx_scale_bytes(rows: int, k: int) -> int:
@@ -429,39 +397,7 @@ def nm_mx_quantize(X: torch.Tensor, Q: torch.Tensor | None = None, S: torch.Tens
                    stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """X [T, k] (fp32 / fp16 / bf16, rows contiguous, any row stride that is a
     multiple of 16 bytes) to microscaled 4-bit codes Q [T, k / 2] and scales S (uint8)."""
-    dt = _MX_DT.get(X.dtype)
-    if dt is None or X.dim() != 2:
-        raise ValueError("X must be a [T, k] float32/float16/bfloat16 tensor with contiguous rows")
-    T, k = X.shape
-    ldx, step = X.stride()
-    if step != 1 and k > 1:
-        raise ValueError("X must be a [T, k] float32/float16/bfloat16 tensor with contiguous rows")
-    if not X.is_cuda or X.get_device() != _current_device():
-        raise ValueError("X must be on the current CUDA device")
-    n = (T + 127) // 128 * ((k + 255) // 256) * 1024
-    if Q is None:
-        Q = _empty((T, k // 2), torch.uint8, X.device, stream)
-    else:
-        _check_tensor("Q", Q, torch.uint8, (T, k // 2))
-    if S is None:
-        S = _empty((n,), torch.uint8, X.device, stream)
-    else:
-        _check_tensor("S", S, torch.uint8, (n,))
-    status = _library().nm_mx_quantize(X.data_ptr(), T, k, ldx if T > 1 else k, dt, Q.data_ptr(), S.data_ptr(),
-                                       _stream(stream))
-    if status:
-        _check(status)
-    return Q, S
-
-
-def _check_mx(Q: torch.Tensor, S: torch.Tensor) -> tuple[int, int]:
-    if Q.dim() != 2:
-        raise ValueError("Q must be [T, k / 2]")
-    T, half = Q.shape
-    k = 2 * half
-    _check_tensor("Q", Q, torch.uint8, (T, half))
-    _check_tensor("S", S, torch.uint8, ((T + 127) // 128 * ((k + 255) // 256) * 1024,))
-    return T, k
+    return (_module or _native()).mx_quantize(X, Q, S, stream)
 
 
 def nm_mx_dequantize(Q: torch.Tensor, S: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
@@ -469,15 +405,7 @@ def nm_mx_dequantize(Q: torch.Tensor, S: torch.Tensor, dtype: torch.dtype = torc
     """The values that codes and scales of ``nm_mx_quantize`` stand for."""
     if dtype not in _MX_DT:
         raise ValueError("dtype must be float32, float16 or bfloat16")
-    T, k = _check_mx(Q, S)
-    if X is None:
-        X = _empty((T, k), dtype, Q.device, stream)
-    else:
-        _check_tensor("X", X, dtype, (T, k))
-    status = _library().nm_mx_dequantize(Q.data_ptr(), S.data_ptr(), T, k, _MX_DT[dtype], X.data_ptr(), _stream(stream))
-    if status:
-        _check(status)
-    return X
+    return (_module or _native()).mx_dequantize(Q, S, _MX_DT[dtype], X, stream)
 
 
 def nm_compress_mx(W: torch.Tensor, N: int = 4, M: int = 4, gated: bool = False, stream=None) -> NMHandle:
@@ -494,21 +422,11 @@ def nm_compress_mx(W: torch.Tensor, N: int = 4, M: int = 4, gated: bool = False,
     return NMHandle(out.value, n_out, k, N, M, NM_MXFP4, gated=bool(gated), src=W.dtype)
 
 
-def _mx_product(name: str, h: NMHandle, Q, S, Y, scale, bias, act: str, out: str, stream) -> torch.Tensor:
-    T, k = _check_mx(Q, S)
-    if k != h.k:
-        raise ValueError(f"Q holds k = {k}, the handle {h.k}")
-    ep = _epilogue(h, scale, bias, act, out, 1.0)
-    want = h.dtype if out == "default" else _OUT_TORCH[out]
-    n = h.n_out // 2 if name == "nm_spmm_mx_gated" else h.n_out
-    if Y is None:
-        Y = _empty((T, n), want, Q.device, stream)
-    else:
-        _check_tensor("Y", Y, want, (T, n))
-    status = getattr(_library(), name)(h.raw, Q.data_ptr(), S.data_ptr(), T, Y.data_ptr(), ep, _stream(stream))
-    if status:
-        _check(status)
-    return Y
+def _mx_product(gated: int, h: NMHandle, Q, S, Y, scale, bias, act: str, out: str, stream) -> torch.Tensor:
+    act_code, out_code = _codes(act, out)
+    src = _MX_DT.get(h.dtype, NM_FP32)  # (a handle of another kind: the library refuses it)
+    return (_module or _native()).spmm_mx(h.raw.value, h.n_out, h.k, src, gated, Q, S, Y, scale, bias, act_code, out_code,
+                                          stream)
 
 
 def nm_spmm_mx(h: NMHandle, Q: torch.Tensor, S: torch.Tensor, Y: torch.Tensor | None = None,
@@ -516,14 +434,14 @@ def nm_spmm_mx(h: NMHandle, Q: torch.Tensor, S: torch.Tensor, Y: torch.Tensor | 
                out: str = "default", stream=None) -> torch.Tensor:
     """Y = out(act(X @ Wm^T * scale + bias)) for a handle of ``nm_compress_mx`` and
     X given as the codes Q and scales S of ``nm_mx_quantize``."""
-    return _mx_product("nm_spmm_mx", h, Q, S, Y, scale, bias, act, out, stream)
+    return _mx_product(0, h, Q, S, Y, scale, bias, act, out, stream)
 
 
 def nm_spmm_mx_gated(h: NMHandle, Q: torch.Tensor, S: torch.Tensor, Y: torch.Tensor | None = None,
                      scale: torch.Tensor | None = None, bias: torch.Tensor | None = None, act: str = "silu",
                      out: str = "default", stream=None) -> torch.Tensor:
     """Y [T, n_out / 2] = act(gate) * up for a gated handle of ``nm_compress_mx``."""
-    return _mx_product("nm_spmm_mx_gated", h, Q, S, Y, scale, bias, act, out, stream)
+    return _mx_product(1, h, Q, S, Y, scale, bias, act, out, stream)
 
 
 def nm_spmm_noalloc(h: NMHandle, X: torch.Tensor, Y: torch.Tensor, scale: torch.Tensor | None = None,

@@ -157,3 +157,25 @@ def test_binding_refuses_before_the_library():
     with pytest.raises(ValueError):
         nm.nm_mx_dequantize(torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(1024, dtype=torch.uint8),
                             dtype=torch.int8)
+
+
+def test_missing_compiled_binding_is_an_error(monkeypatch):
+    import sys
+
+    import torch
+    monkeypatch.setattr(nm, "_module", None)
+    monkeypatch.setitem(sys.modules, nm.__name__ + "._binding", None)
+    monkeypatch.delattr(nm, "_binding", raising=False)
+    with pytest.raises(RuntimeError, match="binding is missing"):
+        nm.nm_mx_quantize(torch.zeros(4, 64))
+
+
+def test_binding_checks_tensors_and_arity():
+    import torch
+    native = nm._native()
+    with pytest.raises(TypeError):
+        native.mx_quantize(torch.zeros(4, 64))
+    with pytest.raises(ValueError, match="must be a tensor"):
+        nm.nm_mx_quantize([1.0, 2.0])
+    with pytest.raises(ValueError, match="CUDA device"):
+        nm.nm_mx_quantize(torch.zeros(4, 64))
