@@ -19,29 +19,38 @@ namespace {
 enum : int { SRC_F16 = NM_FP16, SRC_BF16 = NM_BF16, SRC_F32 = NM_FP32 };
 __host__ __device__ constexpr int src_bytes(int dt) { return dt == SRC_F32 ? 4 : 2; }
 
-// 16 consecutive values as fp32.
+// 16 consecutive values as they lie in memory, and as fp32.
 template <int DT>
-__device__ __forceinline__ void load16(const void* p, float (&v)[16]) {
-  const uint4* q = reinterpret_cast<const uint4*>(p);
+struct Raw16 {
+  uint4 q[src_bytes(DT)];
+  __device__ __forceinline__ void load(const void* p) {
 #pragma unroll
-  for (int i = 0; i < src_bytes(DT); ++i) {
-    const uint4 w = __ldg(q + i);
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    for (int i = 0; i < src_bytes(DT); ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (DT == SRC_F32) {
-        v[4 * i + j] = __uint_as_float(x[j]);
-      } else if constexpr (DT == SRC_BF16) {
-        v[8 * i + 2 * j] = __uint_as_float(x[j] << 16);
-        v[8 * i + 2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
-        v[8 * i + 2 * j] = f.x;
-        v[8 * i + 2 * j + 1] = f.y;
+    for (int i = 0; i < src_bytes(DT); ++i) q[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void to_f32(float (&v)[16]) const {
+#pragma unroll
+    for (int i = 0; i < src_bytes(DT); ++i) {
+      const uint32_t x[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (DT == SRC_F32) {
+          v[4 * i + j] = __uint_as_float(x[j]);
+        } else if constexpr (DT == SRC_BF16) {
+          v[8 * i + 2 * j] = __uint_as_float(x[j] << 16);
+          v[8 * i + 2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
+          v[8 * i + 2 * j] = f.x;
+          v[8 * i + 2 * j + 1] = f.y;
+        }
       }
     }
   }
-}
+};
 
 // Zero all but the N largest magnitudes of every M values (ties keep the lower
 // position): a value goes when N others precede it.
@@ -102,35 +111,35 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const uint8_t* __restr
   const int64_t kk = (int64_t)atom * 128 + (threadIdx.x & 7) * 16;
   const int sub = threadIdx.x >> 3;
   constexpr int PASSES = 4;
-  float v[PASSES][16];
+  Raw16<DT> raw[PASSES];  // every pass's loads are in flight before the first is used
   bool live[PASSES];
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const int64_t r = row0 + i * 32 + sub;
     const int64_t src = r < rows ? (n_ff ? gated_source_row(r, n_ff) : r) : -1;
     live[i] = r < rows && kk < k;
-    if (src >= 0 && kk < k) {
-      load16<DT>(X + src * ldx_bytes + kk * src_bytes(DT), v[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) v[i][j] = 0.0f;
-    }
+    if (src >= 0 && kk < k)
+      raw[i].load(X + src * ldx_bytes + kk * src_bytes(DT));
+    else
+      raw[i].zero();
   }
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
-    prune16<N, M>(v[i]);
+    float v[16];
+    raw[i].to_f32(v);
+    prune16<N, M>(v);
     uint32_t top = 0;  // the largest magnitude, as bits: infinities and NaN compare above all finite values
 #pragma unroll
-    for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
+    for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     const uint32_t eb = top >> 23;  // exponent field: floor(log2) + 127 (0 for subnormals, far below the limit)
     const bool bad = eb == 255u;
     const uint32_t byte = bad ? 255u : (eb > 2u ? eb - 2u : 0u);
     const float inv = bad ? 0.0f : __uint_as_float((254u - byte) << 23);  // 2^-(byte - 127), exact
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[i][j] = bad ? 0.0f : __fmul_rn(v[i][j], inv);
+    for (int j = 0; j < 16; ++j) v[j] = bad ? 0.0f : __fmul_rn(v[j], inv);
     if (live[i]) {
-      const uint2 q = make_uint2(e2m1x8(v[i]), e2m1x8(v[i] + 8));
+      const uint2 q = make_uint2(e2m1x8(v), e2m1x8(v + 8));
       *reinterpret_cast<uint2*>(Q + (row0 + i * 32 + sub) * (k >> 1) + (kk >> 1)) = q;
     }
     if ((threadIdx.x & 1) == 0) sc[sub * 16 + i * 4 + ((threadIdx.x & 7) >> 1)] = live[i] ? (uint8_t)byte : 0;
@@ -141,60 +150,72 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const uint8_t* __restr
         reinterpret_cast<const uint4*>(sc)[threadIdx.x];
 }
 
-// Eight codes to their values (exact in fp16).
-__device__ __forceinline__ void e2m1x8_values(uint32_t q, float* v) {
-  uint32_t h[4];
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(q));
+// Four codes (the low 16 bits of q) to their values.  Every value is an fp16 number
+// whose low byte is zero, so one byte permute with the codes as selectors looks
+// four of them up; the signs are put in place bit by bit.
+__device__ __forceinline__ void e2m1x4_values(uint32_t q, float* v) {
+  // high bytes of 0, 0.5, 1, 1.5 and of 2, 3, 4, 6
+  const uint32_t mag = __byte_perm(0x3E3C3800u, 0x46444240u, q & 0x7777u);
+  const uint32_t sign = ((q << 4) & 0x80u) | ((q << 8) & 0x8000u) | ((q << 12) & 0x800000u) | ((q << 16) & 0x80000000u);
+  const uint32_t hi = mag | sign;
+  const uint32_t h[2] = {__byte_perm(hi, 0u, 0x1404u), __byte_perm(hi, 0u, 0x3424u)};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
     v[2 * i] = f.x;
     v[2 * i + 1] = f.y;
   }
 }
 
-// A thread writes 16 values (half a scale block).  n_ff > 0: packed rows back to
-// their place in W.
+// A thread writes 16 bytes at a time (4 or 8 values), neighbours side by side, so
+// that a warp instruction fills whole sectors.  Block (x, y): `block_rows` rows from
+// row x * block_rows, units [y * cols, (y + 1) * cols) of each (a unit is 16 bytes
+// of output).  n_ff > 0: packed rows back to their place in W.  Memory bound.
 template <int DT>
 __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __restrict__ Q,
                                                             const uint8_t* __restrict__ S, int64_t rows, int64_t k,
-                                                            int64_t n_ff, int64_t n_kb, uint8_t* __restrict__ X) {
+                                                            int64_t n_ff, int64_t n_kb, int block_rows, int cols,
+                                                            uint8_t* __restrict__ X) {
+  constexpr int PER = 16 / src_bytes(DT);  // values of a unit
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t per_row = k / 16;
-  const int64_t unit = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (unit >= rows * per_row) return;
-  const int64_t r = unit / per_row, kk = (unit - r * per_row) * 16;
-  const int64_t dst = n_ff ? gated_source_row(r, n_ff) : r;
-  if (dst < 0) return;
-  const uint2 q = __ldg(reinterpret_cast<const uint2*>(Q + r * (k >> 1) + (kk >> 1)));
-  const uint32_t byte = __ldg(S + mx_scale_offset(r, kk >> 5, n_kb));
-  // 2^(byte - 127): a subnormal for byte 0, NaN for byte 255
-  const float scale = __uint_as_float(byte == 0 ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
-  float v[16];
-  e2m1x8_values(q.x, v);
-  e2m1x8_values(q.y, v + 8);
+  const int64_t row0 = (int64_t)blockIdx.x * block_rows;
+  const int u0 = (int)blockIdx.y * cols, width = min(cols, (int)(k / PER) - u0);
+  const int nrows = (int)min((int64_t)block_rows, rows - row0);
+  // unit c of row dr, advanced by the block's 256 units without a division
+  const int step_r = 256 / width, step_c = 256 - step_r * width;
+  int dr = (int)threadIdx.x / width, c = (int)threadIdx.x - dr * width;
+  const uint8_t* q0 = Q + row0 * (k >> 1) + (int64_t)u0 * (PER / 2);
+#pragma unroll 4
+  for (; dr < nrows; dr += step_r, c += step_c) {
+    if (c >= width) {
+      c -= width;
+      if (++dr >= nrows) break;
+    }
+    const int64_t r = row0 + dr;
+    const int kk = (u0 + c) * PER;
+    const int64_t dst = n_ff ? gated_source_row(r, n_ff) : r;
+    if (dst < 0) continue;
+    const uint8_t* qp = q0 + (int64_t)dr * (k >> 1) + c * (PER / 2);
+    const uint32_t q = PER == 4 ? (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(qp))
+                                : __ldg(reinterpret_cast<const uint32_t*>(qp));
+    const uint32_t byte = __ldg(S + mx_scale_offset(r, kk >> 5, n_kb));
+    // 2^(byte - 127): a subnormal for byte 0, NaN for byte 255
+    const float scale = __uint_as_float(byte == 0 ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
+    float v[PER];
+    e2m1x4_values(q, v);
+    if constexpr (PER == 8) e2m1x4_values(q >> 16, v + 4);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(v[i], scale);
-  uint4* out = reinterpret_cast<uint4*>(X + (dst * k + kk) * src_bytes(DT));
-  if constexpr (DT == SRC_F32) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      out[i] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
-                          __float_as_uint(v[4 * i + 3]));
-  } else {
-    constexpr int OT = DT == SRC_F16 ? OUT_F16 : OUT_BF16;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      out[i] = make_uint4(pack_pair<OT>(v[8 * i], v[8 * i + 1]), pack_pair<OT>(v[8 * i + 2], v[8 * i + 3]),
-                          pack_pair<OT>(v[8 * i + 4], v[8 * i + 5]), pack_pair<OT>(v[8 * i + 6], v[8 * i + 7]));
+    for (int i = 0; i < PER; ++i) v[i] = __fmul_rn(v[i], scale);
+    uint4 o;
+    if constexpr (DT == SRC_F32) {
+      o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    } else {
+      constexpr int OT = DT == SRC_F16 ? OUT_F16 : OUT_BF16;
+      o = make_uint4(pack_pair<OT>(v[0], v[1]), pack_pair<OT>(v[2], v[3]), pack_pair<OT>(v[4], v[5]),
+                     pack_pair<OT>(v[6], v[7]));
+    }
+    *reinterpret_cast<uint4*>(X + (dst * k + kk) * src_bytes(DT)) = o;
   }
 }
 
@@ -232,9 +253,14 @@ cudaError_t launch_quantize_dt(int dt, int N, int M, const void* X, int64_t rows
 template <int DT>
 cudaError_t launch_dequantize(const uint8_t* Q, const uint8_t* S, int64_t rows, int64_t k, int64_t n_ff, void* X,
                               cudaStream_t s) {
-  const int64_t units = rows * (k / 16);
-  return launch_pdl(mx_dequantize_kernel<DT>, dim3((unsigned)((units + 255) / 256)), 256, 0, s, 0, Q, S, rows, k, n_ff,
-                    (k + 255) / 256, static_cast<uint8_t*>(X));
+  const int64_t units = k * src_bytes(DT) / 16;  // of a row
+  const int cols = (int)(units < 2048 ? units : 2048);
+  // as many blocks as are resident at once (8 an SM), of 256 units at least
+  const int64_t chunks = (units + cols - 1) / cols, want = (rows * chunks + 8 * 148 - 1) / (8 * 148);
+  const int block_rows = (int)(want * cols > 256 ? want : (256 + cols - 1) / cols);
+  const dim3 grid((unsigned)((rows + block_rows - 1) / block_rows), (unsigned)((units + cols - 1) / cols));
+  return launch_pdl(mx_dequantize_kernel<DT>, grid, 256, 0, s, 0, Q, S, rows, k, n_ff, (k + 255) / 256, block_rows, cols,
+                    static_cast<uint8_t*>(X));
 }
 
 // ------------------------------------------------------------------ product
@@ -808,7 +834,6 @@ nm_status nm_mx_dequantize(const void* Q, const void* S, int64_t T, int64_t k, n
   const size_t xbytes = (size_t)T * k * (dt == NM_FP32 ? 4 : 2);
   if (overlaps(X, xbytes, Q, (size_t)T * (k / 2)) || overlaps(X, xbytes, S, (size_t)scale_bytes(T, k)))
     return fail(NM_ERR_INVALID, "X overlaps Q or S");
-  if ((T * (k / 16) + 255) / 256 > INT32_MAX) return fail(NM_ERR_UNSUPPORTED, "T x k too large");
   const uint8_t *q = static_cast<const uint8_t*>(Q), *s = static_cast<const uint8_t*>(S);
   cudaError_t e = dt == NM_FP32   ? launch_dequantize<SRC_F32>(q, s, T, k, 0, X, (cudaStream_t)stream)
                   : dt == NM_FP16 ? launch_dequantize<SRC_F16>(q, s, T, k, 0, X, (cudaStream_t)stream)
