@@ -331,8 +331,8 @@ nm_status nm_spmm_gated(const nm_handle* h, const void* X_dev, int64_t T, void* 
  * dX_dev, dW_dev, dbias_dev: any may be NULL (not computed), not all three.
  * X_dev [T][k] (needed for dW only, else may be NULL), P_dev [T][2 n_ff],
  * dY_dev [T][n_ff], all in the handle's type, all pointers 16-byte aligned;
- * k a multiple of 8 (else NM_ERR_UNSUPPORTED).  T == 0 writes zeros to dW and
- * dbias.  ws_dev: device workspace of at least nm_gated_backward_workspace
+ * k a multiple of 8 and T at most 2^26 (else NM_ERR_UNSUPPORTED).  T == 0 writes
+ * zeros to dW and dbias.  ws_dev: device workspace of at least nm_gated_backward_workspace
  * bytes, 16-byte aligned, for this call alone until it has run; calls that
  * overlap need one each.  Outputs and workspace overlap nothing else.
  */

@@ -586,7 +586,9 @@ nm_status check_grad(const nm_handle* h, int64_t T) {
   if (!h->gated || h->mx) return fail(NM_ERR_INVALID, "nm_gated_backward needs a handle made by nm_compress_gated");
   if (h->dt == DT_I8) return fail(NM_ERR_UNSUPPORTED, "gradients are for FP16 and BF16 handles only");
   if (T < 0) return fail(NM_ERR_INVALID, "T must be >= 0 (got %lld)", (long long)T);
-  if (T > (int64_t(1) << 30)) return fail(NM_ERR_UNSUPPORTED, "T above 2^30");
+  // a tile of dW sums over all of T in one go: 2^26 tokens take it a third of the
+  // second that its waits are bounded by
+  if (T > (int64_t(1) << 26)) return fail(NM_ERR_UNSUPPORTED, "T above 2^26");
   return NM_OK;
 }
 

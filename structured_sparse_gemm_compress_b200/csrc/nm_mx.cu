@@ -859,6 +859,7 @@ nm_status nm_compress_mx(const void* W, int64_t n_out, int64_t k, nm_dtype dt, i
   bool sp24 = false;
   if (!pattern_supported(N, M, &sp24)) return fail(NM_ERR_UNSUPPORTED, "N:M %d:%d is not supported", N, M);
   if (!aligned(W, 16)) return fail(NM_ERR_INVALID, "W must be 16-byte aligned");
+  if ((n_out + 159) / 128 * 2 * ((k + 255) / 256) > INT32_MAX) return fail(NM_ERR_UNSUPPORTED, "n_out x k too large");
 
   nm_handle* h = new (std::nothrow) nm_handle();
   if (!h) return fail(NM_ERR_OOM, "host allocation failed");

@@ -426,7 +426,7 @@ def test_refusals_on_a_handle(monkeypatch):
     assert back(x, p, dy, 8, 2, None, None, None, ws, n) == nm.NM_ERR_INVALID        # nothing to compute
     assert back(x, p, dy, 8, 7, dx, dw, None, ws, n) == nm.NM_ERR_INVALID            # unknown activation
     assert back(x, p, dy, -1, 2, dx, dw, None, ws, n) == nm.NM_ERR_INVALID
-    assert back(x, p, dy, (1 << 30) + 1, 2, dx, dw, None, ws, n) == nm.NM_ERR_UNSUPPORTED
+    assert back(x, p, dy, (1 << 26) + 1, 2, dx, dw, None, ws, n) == nm.NM_ERR_UNSUPPORTED
     assert back(x, p, dy, 8, 2, dx, dw, None, ws, need - 1) == nm.NM_ERR_INVALID     # workspace too small
     assert back(x, p, dy, 8, 2, dx, dw, None, None, n) == nm.NM_ERR_INVALID
     assert back(None, p, dy, 8, 2, dx, dw, None, ws, n) == nm.NM_ERR_INVALID
