@@ -399,11 +399,42 @@ __device__ __forceinline__ float gate_value(uint32_t acc, const EpiCh& e, const 
   return f;
 }
 
+// H consecutive tokens of one output channel, the first nvalid of them inside the
+// output; without predicates when the whole run is.
 template <int OT, int H>
 __device__ __forceinline__ void gate_store(const SpmmArgs& a, const float (&y)[H], size_t base, int nvalid) {
+  using T1 = typename std::conditional<
+      OT == OUT_F16, __half,
+      typename std::conditional<OT == OUT_BF16, __nv_bfloat16,
+                                typename std::conditional<OT == OUT_I8, int8_t, float>::type>::type>::type;
+  T1 v[H];
 #pragma unroll
-  for (int j = 0; j < H; ++j)
-    if (j < nvalid) epi_put<OT>(a.Y, base + (size_t)j * a.n_ff, y[j], a.out_scale);
+  for (int j = 0; j < H; j += 2) {
+    if constexpr (OT == OUT_F16) {
+      const __half2 h = __floats2half2_rn(y[j], y[j + 1]);
+      v[j] = h.x;
+      v[j + 1] = h.y;
+    } else if constexpr (OT == OUT_BF16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(y[j], y[j + 1]);
+      v[j] = h.x;
+      v[j + 1] = h.y;
+    } else if constexpr (OT == OUT_I8) {
+      v[j] = (int8_t)rne_sat_s8(__fmul_rn(y[j], a.out_scale));
+      v[j + 1] = (int8_t)rne_sat_s8(__fmul_rn(y[j + 1], a.out_scale));
+    } else {
+      v[j] = y[j];
+      v[j + 1] = y[j + 1];
+    }
+  }
+  T1* p = reinterpret_cast<T1*>(a.Y) + base;
+  if (nvalid >= H) {
+#pragma unroll
+    for (int j = 0; j < H; ++j, p += a.n_ff) *p = v[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < H; ++j, p += a.n_ff)
+      if (j < nvalid) *p = v[j];
+  }
 }
 
 // One warp's run of CH tokens starting at token t0; row: this lane's packed row.
