@@ -1001,10 +1001,16 @@ nm_status compress_rows(const void* W_dev, int64_t n_out, int64_t k, nm_dtype dt
 
   cudaError_t e;
   nm_status st = NM_OK;
-  if ((e = cudaMalloc(&h->d_values, h->values_bytes)) != cudaSuccess) st = cuda_fail(e, "allocate values");
-  else if ((e = cudaMalloc(&h->d_idx, h->idx_bytes)) != cudaSuccess) st = cuda_fail(e, "allocate idx");
-  else if ((e = cudaMalloc(&h->d_bpack, h->bpack_bytes)) != cudaSuccess) st = cuda_fail(e, "allocate packed image");
-  else if ((e = cudaMalloc(&h->d_err, sizeof(int))) != cudaSuccess) st = cuda_fail(e, "allocate error word");
+  nm::Arena arena;
+  const size_t at_values = arena.add(h->values_bytes), at_idx = arena.add(h->idx_bytes);
+  const size_t at_bpack = arena.add(h->bpack_bytes), at_err = arena.add(sizeof(int));
+  if ((e = arena.allocate(h)) == cudaSuccess) {
+    h->d_values = arena.base + at_values;
+    h->d_idx = arena.base + at_idx;
+    h->d_bpack = arena.base + at_bpack;
+    h->d_err = reinterpret_cast<int*>(arena.base + at_err);
+  }
+  if (e != cudaSuccess) st = cuda_fail(e, "allocate the compressed weight");
   else if ((e = cudaMemsetAsync(h->d_err, 0, sizeof(int), (cudaStream_t)stream)) != cudaSuccess)
     st = cuda_fail(e, "clear error word");
   else if ((e = nm::launch_compress(h, W_dev, (cudaStream_t)stream)) != cudaSuccess)
@@ -1211,13 +1217,15 @@ nm_status nm_spmm_noalloc(const nm_handle* h, const void* X, int64_t T, void* Y,
 void nm_destroy(nm_handle* h) {
   if (!h) return;
   cudaDeviceSynchronize();
-  cudaFree(h->d_values);
-  cudaFree(h->d_idx);
-  cudaFree(h->d_bpack);
-  cudaFree(h->d_kidx);
-  cudaFree(h->d_mxq);
-  cudaFree(h->d_mxs);
-  cudaFree(h->d_err);
+  if (h->d_arena) {
+    cudaFree(h->d_arena);
+  } else {  // nm_compress_tile: one allocation per buffer
+    cudaFree(h->d_values);
+    cudaFree(h->d_idx);
+    cudaFree(h->d_bpack);
+    cudaFree(h->d_kidx);
+    cudaFree(h->d_err);
+  }
   cudaFree(h->d_ws);
   cudaFree(h->d_cnt);
   delete h;

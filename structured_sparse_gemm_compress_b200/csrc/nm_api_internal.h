@@ -19,6 +19,22 @@ int num_sms(int dev);
 nm_status check_handle(const nm_handle* h);
 // Whether the library prunes to N:M (sp24: on the 2:4 sparse tensor core).
 bool pattern_supported(int N, int M, bool* sp24);
+// One device allocation for several buffers of a handle: sizes are added first,
+// then allocated, then handed out in the same order (256-byte aligned).
+struct Arena {
+  size_t total = 0;
+  uint8_t* base = nullptr;
+  size_t add(size_t bytes) {
+    const size_t at = total;
+    total += (bytes + 255) / 256 * 256;
+    return at;
+  }
+  cudaError_t allocate(nm_handle* h) {
+    cudaError_t e = cudaMalloc(&h->d_arena, total);
+    base = static_cast<uint8_t*>(h->d_arena);
+    return e;
+  }
+};
 // [a, a + an) and [b, b + bn) share a byte.
 inline bool overlaps(const void* a, size_t an, const void* b, size_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);

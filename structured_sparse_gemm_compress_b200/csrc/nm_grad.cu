@@ -155,24 +155,26 @@ __global__ void __launch_bounds__(32 * kDpWarps, BIAS ? 3 : 4)
   }
 }
 
-// dbias: one warp adds up the row blocks' sums of 32 columns, as eight interleaved
-// runs (eight loads in flight) that are then added in order.
-__device__ __forceinline__ void dbias_columns(const float* __restrict__ part, int n, int row_blocks, int c,
+// dbias: a warp adds up the row blocks' sums of four columns, its eight groups of
+// four lanes every eighth row block each (eight loads in flight a lane), then the
+// groups pairwise: a fixed order whatever the launch.
+__device__ __forceinline__ void dbias_columns(const float* __restrict__ part, int n, int row_blocks, int c0, int lane,
                                               float* __restrict__ dbias) {
-  if (c >= n) return;
+  const int c = c0 + (lane & 3), group = lane >> 2;
   float run[8] = {};
-  int b = 0;
-  for (; b + 8 <= row_blocks; b += 8) {
+  if (c < n) {
+    for (int b = group; b < row_blocks; b += 64) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) run[i] += __ldg(part + (size_t)(b + i) * n + c);
+      for (int i = 0; i < 8; ++i)
+        if (b + 8 * i < row_blocks) run[i] += __ldg(part + (size_t)(b + 8 * i) * n + c);
+    }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (b + i < row_blocks) run[i] += __ldg(part + (size_t)(b + i) * n + c);
   float s = run[0];
 #pragma unroll
   for (int i = 1; i < 8; ++i) s += run[i];
-  dbias[c] = s;
+#pragma unroll
+  for (int d = 4; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  if (group == 0 && c < n) dbias[c] = s;
 }
 
 // The launch of a call that asks for nothing else; otherwise the products' idle
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(128) dbias_kernel(const float* __restrict__ pa
                                                     float* __restrict__ dbias) {
   pdl_launch_dependents();
   pdl_wait();
-  dbias_columns(part, n, row_blocks, (int)(blockIdx.x * blockDim.x + threadIdx.x), dbias);
+  dbias_columns(part, n, row_blocks, (int)(blockIdx.x * 4 + (threadIdx.x >> 5)) * 4, threadIdx.x & 31, dbias);
 }
 
 // ------------------------------------------------------------------ the two products
@@ -220,6 +222,8 @@ struct GradSide {
   int dw;            // 1: dW, 0: dX
   int n_kb;          // stages per tile
   int n_mt;          // row tiles (dW: of one half)
+  int splits;        // parts of a tile's sum (split launches), of `per_split` stages
+  int per_split;
 };
 
 struct GradArgs {
@@ -228,6 +232,11 @@ struct GradArgs {
   int hi_tiles, lo_tiles;  // tiles of side 1 for those pairs, and for the others
   int F, T, k;
   int kb_half;       // dX: stages per half of 2 n_ff
+  // Split launch: fewer tiles than pairs and long sums.  Every unit is one part of a
+  // tile's sum and has a pair of its own; the parts leave their fp32 tiles in
+  // `partial` ([unit][256][BN]) and grad_join_kernel adds them up.
+  int split;
+  float* partial;
   void *dW, *dX;
   const float* part;       // with dbias: the row blocks' column sums, row_blocks of them
   float* dbias;
@@ -237,7 +246,9 @@ struct GradArgs {
 };
 
 struct GradUnit {
-  int dw, m0, n0, z, n_kb;
+  int dw, m0, n0, z;
+  int kb0, kb1;           // stages of the sum
+  int splits;             // split launch: parts of the tile
 };
 
 // The i-th unit of this pair; false when there is none.  Side 0's tiles go round
@@ -246,8 +257,15 @@ struct GradUnit {
 // over all (hi_tiles <= lo_tiles), the last round cut off at the end of the list.
 __device__ __forceinline__ bool grad_unit(const GradArgs& a, int pair, int pairs, int i, int bn, GradUnit& u) {
   const int q = a.side[0].tiles / pairs + (pair < a.hi ? 1 : 0);
-  int s = 0, tile;
-  if (i < q) {
+  int s = 0, tile, z = 0;
+  if (a.split) {
+    if (i > 0) return false;
+    const int n0 = a.side[0].tiles * a.side[0].splits;
+    s = pair >= n0 ? 1 : 0;
+    const int unit = pair - s * n0;
+    tile = unit / a.side[s].splits;
+    z = unit - tile * a.side[s].splits;
+  } else if (i < q) {
     tile = i * pairs + pair;
   } else {
     s = 1;
@@ -270,7 +288,9 @@ __device__ __forceinline__ bool grad_unit(const GradArgs& a, int pair, int pairs
   const GradSide& g = a.side[s];
   const int nt = tile % g.n_nt, mt = tile / g.n_nt;
   u.dw = g.dw;
-  u.n_kb = g.n_kb;
+  u.splits = a.split ? g.splits : 1;
+  u.kb0 = a.split ? z * g.per_split : 0;
+  u.kb1 = a.split ? min(g.n_kb, u.kb0 + g.per_split) : g.n_kb;
   u.n0 = nt * bn;
   u.z = g.dw ? mt / g.n_mt : 0;
   u.m0 = (g.dw ? mt % g.n_mt : mt) * 256;
@@ -345,7 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     bool ok = true;
     for (int i = 0; ok && grad_unit(a, pair, pairs, i, BN, u); ++i) {
       const int m = u.m0 + (int)rank * 128, n = u.n0 + (int)rank * (BN / 2);
-      for (int kb = 0; kb < u.n_kb; ++kb) {
+      for (int kb = u.kb0; kb < u.kb1; ++kb) {
         if (!mbar_wait_warp(&empty_bar[stage], phase ^ 1u, &abort_sh, tmo)) {
           if (issuer) give_up(1);
           ok = false;
@@ -398,7 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         const uint32_t idesc = u.dw ? grad_idesc<DT, BN>(true) : grad_idesc<DT, BN>(false);
         // per MMA (16 summed elements): 32 bytes along a K-major row, 16 rows of an MN-major run
         const uint64_t a_step = u.dw ? (16u * 128u) >> 4 : 32u >> 4, b_step = (16u * 128u) >> 4;
-        for (int kb = 0; kb < u.n_kb; ++kb) {
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
           if (!mbar_wait_warp(&full_bar[stage], phase, &abort_sh, tmo)) {
             if (issuer) give_up(3);
             ok = false;
@@ -411,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
           if (issuer) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              tc_mma_pair<1>(d_tmem, ad0 + a_step * j, bd0 + b_step * j, idesc, (kb > 0 || j > 0) ? 1u : 0u);
+              tc_mma_pair<1>(d_tmem, ad0 + a_step * j, bd0 + b_step * j, idesc, (kb > u.kb0 || j > 0) ? 1u : 0u);
             tc_commit_pair(&empty_bar[stage], (uint16_t)3);
           }
           if (++stage == C::STAGES) {
@@ -435,48 +455,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     const int ew = warp - 2, lq = warp & 3, part = ew >> 2;
     uint8_t* buf = smem + (size_t)C::STAGES * C::STAGE + (size_t)ew * C::EPI_BUF;
     if (a.dbias)  // while the first tile is summed
-      for (int c = ((int)blockIdx.x * kGradEpiWarps + ew) * 32; c < 2 * a.F; c += (int)gridDim.x * kGradEpiWarps * 32)
-        dbias_columns(a.part, 2 * a.F, a.row_blocks, c + lane, a.dbias);
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    for (int i = 0; grad_unit(a, pair, pairs, i, BN, u); ++i) {
-      if (!mbar_wait_warp(&accf_bar[acc], acc_phase, &abort_sh, tmo)) {
-        if (lane == 0) give_up(4);
-        break;
-      }
-      tc_fence_after();
-      const int row0 = u.m0 + (int)rank * 128 + lq * 32, col0 = u.n0 + part * C::WCOLS;
-      const int rows = min(32, (u.dw ? a.F : a.T) - row0);
-      uint8_t* out = static_cast<uint8_t*>(u.dw ? a.dW : a.dX) +
-                     ((int64_t)(u.dw ? u.z * a.F : 0) + row0) * a.k * 2;
-      const uint32_t taddr = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * BN + part * C::WCOLS);
+      for (int c = ((int)blockIdx.x * kGradEpiWarps + ew) * 4; c < 2 * a.F; c += (int)gridDim.x * kGradEpiWarps * 4)
+        dbias_columns(a.part, 2 * a.F, a.row_blocks, c, lane, a.dbias);
+    if (a.split && grad_unit(a, pair, pairs, 0, BN, u) && u.splits > 1) {
+      if (mbar_wait_warp(&accf_bar[0], 0, &abort_sh, tmo)) {
+        tc_fence_after();
+        const int r0 = lq * 32, c0 = part * C::WCOLS;
+        const uint32_t taddr = tmem + ((uint32_t)r0 << 16) + (uint32_t)c0;
+        float* mine = a.partial + ((size_t)pair * 256 + (size_t)rank * 128 + r0) * BN + c0;
 #pragma unroll 1
-      for (int c = 0; c < C::WCOLS; c += 64) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t r[32];
-          __syncwarp();
-          tmem_ld32(taddr + (uint32_t)(c + 32 * h), r);
-          tmem_wait_ld();
-          if (h == 1 && c + 64 == C::WCOLS) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(acce_lead0 + 8u * (uint32_t)acc);
-          }
+        for (int c = 0; c < C::WCOLS; c += 32) {
           float v[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-          stage_row<OT, 128, 32>(buf, (uint32_t)lane, (uint32_t)(4 * h), v);
+          __syncwarp();
+          tmem_ld32(taddr + (uint32_t)c, *reinterpret_cast<uint32_t(*)[32]>(v));
+          tmem_wait_ld();
+          stage_row<OUT_F32, 128, 32>(buf, (uint32_t)lane, 0, v);
+          __syncwarp();
+          stage_flush<128, 4>(buf, reinterpret_cast<uint8_t*>(mine + c), (int64_t)BN * 4, 32, 128, true, lane);
+          __syncwarp();
         }
-        __syncwarp();
-        if (rows > 0 && col0 + c < a.k)
-          stage_flush<128, 2>(buf, out + (int64_t)(col0 + c) * 2, (int64_t)a.k * 2, rows, min(64, a.k - col0 - c) * 2,
-                              true, lane);
-        __syncwarp();
+      } else if (lane == 0) {
+        give_up(4);
       }
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1u;
+    } else {
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      for (int i = 0; grad_unit(a, pair, pairs, i, BN, u); ++i) {
+        if (!mbar_wait_warp(&accf_bar[acc], acc_phase, &abort_sh, tmo)) {
+          if (lane == 0) give_up(4);
+          break;
+        }
+        tc_fence_after();
+        const int row0 = u.m0 + (int)rank * 128 + lq * 32, col0 = u.n0 + part * C::WCOLS;
+        const int rows = min(32, (u.dw ? a.F : a.T) - row0);
+        uint8_t* out = static_cast<uint8_t*>(u.dw ? a.dW : a.dX) +
+                       ((int64_t)(u.dw ? u.z * a.F : 0) + row0) * a.k * 2;
+        const uint32_t taddr = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * BN + part * C::WCOLS);
+#pragma unroll 1
+        for (int c = 0; c < C::WCOLS; c += 64) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            __syncwarp();
+            tmem_ld32(taddr + (uint32_t)(c + 32 * h), r);
+            tmem_wait_ld();
+            if (h == 1 && c + 64 == C::WCOLS) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster_relaxed(acce_lead0 + 8u * (uint32_t)acc);
+            }
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+            stage_row<OT, 128, 32>(buf, (uint32_t)lane, (uint32_t)(4 * h), v);
+          }
+          __syncwarp();
+          if (rows > 0 && col0 + c < a.k)
+            stage_flush<128, 2>(buf, out + (int64_t)(col0 + c) * 2, (int64_t)a.k * 2, rows, min(64, a.k - col0 - c) * 2,
+                                true, lane);
+          __syncwarp();
+        }
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
       }
     }
   }
@@ -490,6 +532,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
   }
 }
 
+// Adds up the parts of split tiles, in order, and rounds once.  A block takes eight
+// rows of one tile (blockIdx.y), a warp a row of it, a lane four columns at a time;
+// eight parts' loads are in flight.
+template <int DT, int BN>
+__global__ void __launch_bounds__(256) grad_join_kernel(const GradArgs a) {
+  constexpr int OT = DT == DT_F16 ? OUT_F16 : OUT_BF16;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int t0 = a.side[0].splits > 1 ? a.side[0].tiles : 0;  // split tiles of side 0 come first
+  const int s = (int)blockIdx.y >= t0 ? 1 : 0, tile = (int)blockIdx.y - s * t0;
+  const GradSide& g = a.side[s];
+  const int first = s * a.side[0].tiles * a.side[0].splits + tile * g.splits;
+  const int nt = tile % g.n_nt, mt = tile / g.n_nt, z = g.dw ? mt / g.n_mt : 0;
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), m = (g.dw ? mt % g.n_mt : mt) * 256 + row;
+  if (m >= (g.dw ? a.F : a.T)) return;
+  uint16_t* out = static_cast<uint16_t*>(g.dw ? a.dW : a.dX) + ((int64_t)(z * a.F) + m) * a.k;
+  for (int c = (threadIdx.x & 31) * 4; c < BN && nt * BN + c < a.k; c += 128) {
+    const float* src = a.partial + ((size_t)first * 256 + row) * BN + c;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int p = 0; p < g.splits; ++p) {
+      const float4 w = *reinterpret_cast<const float4*>(src + (size_t)p * 256 * BN);
+      v.x += w.x;
+      v.y += w.y;
+      v.z += w.z;
+      v.w += w.w;
+    }
+    *reinterpret_cast<uint2*>(out + nt * BN + c) = make_uint2(pack_pair<OT>(v.x, v.y), pack_pair<OT>(v.z, v.w));
+  }
+}
+
 struct GradMaps {
   CUtensorMap pw, px, x, w;
 };
@@ -500,7 +573,10 @@ cudaError_t launch_grad_t(int grid, const GradMaps& m, const GradArgs& a, cudaSt
   static std::atomic<uint64_t> opted{0};
   cudaError_t e = smem_opt_in(kern, GradCfg<BN>::SMEM, opted);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3((unsigned)(2 * grid)), kGradThreads, GradCfg<BN>::SMEM, s, 0, m.pw, m.px, m.x, m.w, a);
+  e = launch_pdl(kern, dim3((unsigned)(2 * grid)), kGradThreads, GradCfg<BN>::SMEM, s, 0, m.pw, m.px, m.x, m.w, a);
+  if (e != cudaSuccess || !a.split) return e;
+  const int tiles = (a.side[0].splits > 1 ? a.side[0].tiles : 0) + (a.side[1].splits > 1 ? a.side[1].tiles : 0);
+  return tiles ? launch_pdl(grad_join_kernel<DT, BN>, dim3(32, (unsigned)tiles), 256, 0, s, 0, a) : cudaSuccess;
 }
 
 // Rows per block: eight a warp, or two when that would leave SMs without a block
@@ -525,22 +601,8 @@ cudaError_t launch_dp(bool vec, const void* P, const void* dY, int T, int F, int
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// Workspace: dp, the masked dense weight, the row blocks' column sums.
-struct GradWs {
-  int64_t pitch, dp, wm, part, total;
-  GradWs(const nm_handle* h, int64_t T) {
-    const int64_t F = h->n_out / 2;
-    pitch = (F + 63) / 64 * 64;  // whole 128-byte lines: a 128-byte box row then touches one
-    dp = 0;
-    wm = dp + align256(T * 2 * pitch * 2);
-    part = wm + align256(h->n_out * h->k * 2);
-    const int64_t rows = dp_block_rows(T, F);
-    total = part + align256((T + rows - 1) / rows * h->n_out * 4);
-  }
-};
-
-// Tiles of both products for tiles bn columns wide, shared out over at most
-// `pairs` CTA pairs: side 0 (the longer sums) goes round the pairs, side 1 goes on
+// The launch for tiles bn columns wide on at most `pairs` CTA pairs.  Unless the
+// sums are split, side 0 (the longer sums) goes round the pairs and side 1 goes on
 // top so that the fullest pair has the least to do.  Returns that pair's stages
 // (with a fixed part per tile), -1 when there are too many tiles.
 int64_t plan_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw, int bn, int pairs, GradArgs* a, int* grid) {
@@ -562,6 +624,7 @@ int64_t plan_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw, int
   if (w_tiles > INT32_MAX / 2 || x_tiles > INT32_MAX / 2) return -1;
   sw.tiles = (int)w_tiles;
   sx.tiles = (int)x_tiles;
+  sw.splits = sx.splits = 1;
   const bool w_first = sw.n_kb >= sx.n_kb;
   a->side[0] = w_first ? sw : sx;
   a->side[1] = w_first ? sx : sw;
@@ -577,7 +640,88 @@ int64_t plan_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw, int
   }
   a->lo_tiles = (int)lo;
   a->hi_tiles = (int)hi;
-  return std::max(q * c0 + lo * c1, a->hi ? (q + 1) * c0 + hi * c1 : 0);
+  int64_t cost = std::max(q * c0 + lo * c1, a->hi ? (q + 1) * c0 + hi * c1 : 0);
+  if (w_tiles + x_tiles >= pairs) return cost;
+
+  // Fewer tiles than pairs: cut the sums into parts of at most `len` stages, one
+  // part per pair.  Joining them (fp32 tiles out to L2, another launch) costs about
+  // kJoin stages.
+  constexpr int kJoin = 24;
+  const char* whole = getenv("NMSPMM_GRAD_SPLIT");  // 0: no split (tests and sweeps)
+  if (whole && whole[0] == '0') return cost;
+  for (int len = 8; len < a->side[0].n_kb || len < a->side[1].n_kb; len += len / 4) {
+    int64_t units = 0;
+    int split[2], per[2];
+    for (int i = 0; i < 2; ++i) {
+      const int n = a->side[i].n_kb;
+      split[i] = (n + len - 1) / len;
+      per[i] = (n + split[i] - 1) / split[i];
+      split[i] = (n + per[i] - 1) / per[i];  // no part is empty
+      units += (int64_t)a->side[i].tiles * split[i];
+    }
+    if (units > pairs) continue;
+    const int64_t c = len + kFixed + kJoin;
+    if (c < cost) {
+      cost = c;
+      a->split = 1;
+      *grid = (int)units;
+      for (int i = 0; i < 2; ++i) {
+        a->side[i].splits = split[i];
+        a->side[i].per_split = per[i];
+      }
+    }
+  }
+  return cost;
+}
+
+// Workspace: dp, the masked dense weight, the row blocks' column sums, and for
+// split launches their partial tiles (a unit per pair at most).
+struct GradWs {
+  int64_t pitch, dp, wm, part, partial, total;
+  bool may_split;
+  GradWs(const nm_handle* h, int64_t T) {
+    const int64_t F = h->n_out / 2, pairs = num_sms(h->device) / 2;
+    pitch = (F + 63) / 64 * 64;  // whole 128-byte lines: a 128-byte box row then touches one
+    dp = 0;
+    wm = dp + align256(T * 2 * pitch * 2);
+    part = wm + align256(h->n_out * h->k * 2);
+    const int64_t rows = dp_block_rows(T, F);
+    partial = part + align256((T + rows - 1) / rows * h->n_out * 4);
+    // a 128-wide tiling with as many tiles as pairs is not split, nor is any wider one then
+    const int64_t n_nt = (h->k + 127) / 128, tiles = std::min(2 * ((F + 255) / 256), (T + 255) / 256) * n_nt;
+    may_split = tiles < 2 * pairs;
+    total = partial + (may_split ? pairs * 256 * 256 * 4 : 0);
+  }
+};
+
+int forced_grad_bn() {  // tests and sweeps
+  const char* v = getenv("NMSPMM_FORCE_GRAD_BN");
+  return v && *v ? atoi(v) : 0;
+}
+
+// The tile width with the lower estimate of the fullest pair's work, and its
+// launch.  A stage of a 256-wide tile takes 1.45 times a 128-wide one's (0.33
+// against 0.23 us over full waves, 0.28 against 0.19 when few tiles run; the
+// narrower tile moves 24 KB a stage and SM against 32 KB for half the products).
+nm_status choose_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw, GradArgs* a, int* grid, int* bn) {
+  const int pairs = num_sms(h->device) / 2, forced = forced_grad_bn();
+  *bn = 0;
+  double best = 1e300;
+  for (int w : {256, 128}) {
+    if (forced && w != forced) continue;
+    GradArgs c{};
+    int g = 0;
+    const int64_t level = plan_grad(h, T, want_dx, want_dw, w, pairs, &c, &g);
+    if (level < 0) return fail(NM_ERR_UNSUPPORTED, "T x k too large");
+    const double cost = (double)level * (w == 256 ? 1.45 : 1.0);
+    if (cost < best) {
+      best = cost;
+      *a = c;
+      *bn = w;
+      *grid = g;
+    }
+  }
+  return *bn ? NM_OK : fail(NM_ERR_INVALID, "NMSPMM_FORCE_GRAD_BN must be 128 or 256");
 }
 
 nm_status check_grad(const nm_handle* h, int64_t T) {
@@ -669,6 +813,10 @@ nm_status nm_gated_backward(const nm_handle* h, const void* X, const void* P, co
   }
   if ((int64_t)row_blocks * ((F + kDpCols - 1) / kDpCols) + un.blocks > INT32_MAX)
     return fail(NM_ERR_UNSUPPORTED, "T x n_ff too large");
+  GradArgs a{};
+  int bn = 0, grid = 0;
+  if ((dX || dW) && (st = choose_grad(h, T, dX != nullptr, dW != nullptr, &a, &grid, &bn)) != NM_OK) return st;
+  if (a.split && !lay.may_split) return fail(NM_ERR_INVALID, "the workspace has no room for a split launch");
   cudaError_t e = cudaSuccess;
   const bool vec = F % 8 == 0;  // every row starts on 16 bytes
   e = h->dt == DT_F16 ? launch_dp<DT_F16>(vec, P, dY, (int)T, (int)F, (int)lay.pitch, (int)act, dp, part, un, s)
@@ -676,31 +824,7 @@ nm_status nm_gated_backward(const nm_handle* h, const void* X, const void* P, co
   if (e != cudaSuccess) return cuda_fail(e, "launch the gradient of the output stage");
 
   if (dX || dW) {
-    const int pairs = num_sms(h->device) / 2;
-    // Tile width: the lower estimate of the fullest pair's work.  A stage of a
-    // 256-wide tile takes 1.45 times a 128-wide one's (0.33 against 0.23 us over
-    // full waves, 0.28 against 0.19 when few tiles run; the narrower tile moves
-    // 24 KB a stage and SM against 32 KB for half the products).
-    GradArgs a{};
-    int bn = 0, grid = 0;
-    double best = 1e300;
-    const char* forced = getenv("NMSPMM_FORCE_GRAD_BN");  // tests and sweeps
-    const int forced_bn = forced && *forced ? atoi(forced) : 0;
-    for (int w : {256, 128}) {
-      if (forced_bn && w != forced_bn) continue;
-      GradArgs c{};
-      int g = 0;
-      const int64_t level = plan_grad(h, T, dX != nullptr, dW != nullptr, w, pairs, &c, &g);
-      if (level < 0) return fail(NM_ERR_UNSUPPORTED, "T x k too large");
-      const double cost = (double)level * (w == 256 ? 1.45 : 1.0);
-      if (cost < best) {
-        best = cost;
-        a = c;
-        bn = w;
-        grid = g;
-      }
-    }
-    if (!bn) return fail(NM_ERR_INVALID, "NMSPMM_FORCE_GRAD_BN must be 128 or 256");
+    a.partial = reinterpret_cast<float*>(base + lay.partial);
     a.dW = dW;
     a.dX = dX;
     a.part = part;
@@ -725,7 +849,7 @@ nm_status nm_gated_backward(const nm_handle* h, const void* X, const void* P, co
     if (e != cudaSuccess) return cuda_fail(e, "launch the gradient products");
   }
   if (dbias && !dX && !dW) {
-    e = launch_pdl(dbias_kernel, dim3((unsigned)((h->n_out + 127) / 128)), 128, 0, s, 0, (const float*)part,
+    e = launch_pdl(dbias_kernel, dim3((unsigned)((h->n_out + 15) / 16)), 128, 0, s, 0, (const float*)part,
                    (int)h->n_out, row_blocks, dbias);
     if (e != cudaSuccess) return cuda_fail(e, "launch the bias gradient");
   }

@@ -19,6 +19,10 @@ struct nm_handle {
   size_t chunk = 0;      // bytes per (channel tile, k-block) chunk
   int device = 0;
 
+  // One allocation behind the pointers below where the handle has it (nm_compress,
+  // nm_compress_gated, nm_compress_mx: a cudaMalloc takes longer than the packing).
+  void* d_arena = nullptr;
+
   void* d_values = nullptr;   // canonical values [n_out][k/M][N]
   uint8_t* d_idx = nullptr;   // canonical 4-bit positions [n_out][idx_pitch]
   size_t values_bytes = 0, idx_bytes = 0;

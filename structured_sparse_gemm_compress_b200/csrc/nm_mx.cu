@@ -876,9 +876,14 @@ nm_status nm_compress_mx(const void* W, int64_t n_out, int64_t k, nm_dtype dt, i
   h->mxs_bytes = (size_t)scale_bytes(h->mx_rows, k);
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
-  if ((e = cudaMalloc(&h->d_mxq, (size_t)h->mx_rows * (k / 2))) != cudaSuccess) st = cuda_fail(e, "allocate codes");
-  else if ((e = cudaMalloc(&h->d_mxs, h->mxs_bytes)) != cudaSuccess) st = cuda_fail(e, "allocate scales");
-  else if ((e = cudaMalloc(&h->d_err, sizeof(int))) != cudaSuccess) st = cuda_fail(e, "allocate error word");
+  Arena arena;
+  const size_t at_q = arena.add((size_t)h->mx_rows * (k / 2)), at_s = arena.add(h->mxs_bytes), at_err = arena.add(sizeof(int));
+  if ((e = arena.allocate(h)) == cudaSuccess) {
+    h->d_mxq = arena.base + at_q;
+    h->d_mxs = arena.base + at_s;
+    h->d_err = reinterpret_cast<int*>(arena.base + at_err);
+  }
+  if (e != cudaSuccess) st = cuda_fail(e, "allocate the quantised weight");
   else if ((e = cudaMemsetAsync(h->d_err, 0, sizeof(int), s)) != cudaSuccess) st = cuda_fail(e, "clear error word");
   else if ((e = launch_mx_pack(h, W, s)) != cudaSuccess) st = cuda_fail(e, "launch the quantisation");
   for (int i = 0; i < 3 && st == NM_OK; ++i) st = codes_map(&h->tm_mxq[i], h->d_mxq, h->mx_rows, k, kMxTiles[i] / 2);

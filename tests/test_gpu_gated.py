@@ -39,7 +39,7 @@ ACTS = ["none", "gelu", "silu", "relu"]
 @pytest.fixture(autouse=True)
 def _no_forced_plan(monkeypatch):
     for k in ("NMSPMM_FORCE_BN", "NMSPMM_FORCE_SPLITK", "NMSPMM_FORCE_XS", "NMSPMM_FORCE_GRID",
-              "NMSPMM_FORCE_PAIR", "NMSPMM_SPLIT_GLOBAL", "NMSPMM_FORCE_GRAD_BN"):
+              "NMSPMM_FORCE_PAIR", "NMSPMM_SPLIT_GLOBAL", "NMSPMM_FORCE_GRAD_BN", "NMSPMM_GRAD_SPLIT"):
         monkeypatch.delenv(k, raising=False)
 
 
@@ -275,6 +275,19 @@ def test_backward_many_tiles(monkeypatch, T, k, F, bn):
     """More tiles than CTA pairs, each product in turn the one with the longer sums; both tile widths."""
     monkeypatch.setenv("NMSPMM_FORCE_GRAD_BN", str(bn))
     check_backward("bf16", T, k, F, act="gelu", seed=1)
+
+
+@pytest.mark.parametrize("bn", [128, 256])
+@pytest.mark.parametrize("T,k,F", [(200, 264, 1030), (3000, 64, 40), (1500, 136, 700), (1, 512, 2048)])
+def test_backward_split_sums(monkeypatch, T, k, F, bn):
+    """Few tiles with long sums: parts of a tile's sum on several pairs, the same result every time."""
+    monkeypatch.setenv("NMSPMM_FORCE_GRAD_BN", str(bn))
+    h, X, P, dY, (dX, dW, db) = check_backward("bf16", T, k, F, seed=T)
+    for _ in range(10):
+        x, w, b = nm.nm_gated_backward(h, X.cuda(), P.cuda(), dY.cuda(), bias_grad=True)
+        assert torch.equal(x, dX) and torch.equal(w, dW) and torch.equal(b, db)
+    monkeypatch.setenv("NMSPMM_GRAD_SPLIT", "0")
+    check_backward("bf16", T, k, F, seed=T)
 
 
 def test_backward_parts_and_repeats():
