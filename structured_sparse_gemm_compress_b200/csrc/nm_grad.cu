@@ -222,20 +222,19 @@ struct GradSide {
   int dw;            // 1: dW, 0: dX
   int n_kb;          // stages per tile
   int n_mt;          // row tiles (dW: of one half)
-  int splits;        // parts of a tile's sum (split launches), of `per_split` stages
+  int splits;        // parts of a tile's sum, of `per_split` stages: units = tiles * splits
   int per_split;
+  int slot0;         // splits > 1: where its units' partial tiles start
 };
 
 struct GradArgs {
   GradSide side[2];
-  int hi;                  // pairs with one more tile of side 0 than the others
-  int hi_tiles, lo_tiles;  // tiles of side 1 for those pairs, and for the others
+  int hi;                  // pairs with one more unit of side 0 than the others
+  int hi_units, lo_units;  // units of side 1 for those pairs, and for the others
   int F, T, k;
   int kb_half;       // dX: stages per half of 2 n_ff
-  // Split launch: fewer tiles than pairs and long sums.  Every unit is one part of a
-  // tile's sum and has a pair of its own; the parts leave their fp32 tiles in
-  // `partial` ([unit][256][BN]) and grad_join_kernel adds them up.
-  int split;
+  // Where few tiles have long sums, a tile is cut into parts on several pairs: they
+  // leave fp32 tiles in `partial` ([slot][256][BN]) and grad_join_kernel adds them up.
   float* partial;
   void *dW, *dX;
   const float* part;       // with dbias: the row blocks' column sums, row_blocks of them
@@ -247,50 +246,45 @@ struct GradArgs {
 
 struct GradUnit {
   int dw, m0, n0, z;
-  int kb0, kb1;           // stages of the sum
-  int splits;             // split launch: parts of the tile
+  int kb0, kb1;  // stages of the sum
+  int slot;      // part of a split tile: where its fp32 tile goes; else -1
 };
 
-// The i-th unit of this pair; false when there is none.  Side 0's tiles go round
+// The i-th unit of this pair; false when there is none.  Side 0's units go round
 // the pairs; `hi` pairs get one more of them than the others.  Side 1's: first
-// lo_tiles - hi_tiles rounds over the other pairs alone, then hi_tiles rounds
-// over all (hi_tiles <= lo_tiles), the last round cut off at the end of the list.
+// lo_units - hi_units rounds over the other pairs alone, then hi_units rounds
+// over all (hi_units <= lo_units), the last round cut off at the end of the list.
 __device__ __forceinline__ bool grad_unit(const GradArgs& a, int pair, int pairs, int i, int bn, GradUnit& u) {
-  const int q = a.side[0].tiles / pairs + (pair < a.hi ? 1 : 0);
-  int s = 0, tile, z = 0;
-  if (a.split) {
-    if (i > 0) return false;
-    const int n0 = a.side[0].tiles * a.side[0].splits;
-    s = pair >= n0 ? 1 : 0;
-    const int unit = pair - s * n0;
-    tile = unit / a.side[s].splits;
-    z = unit - tile * a.side[s].splits;
-  } else if (i < q) {
-    tile = i * pairs + pair;
+  const int n0 = a.side[0].tiles * a.side[0].splits;
+  const int q = n0 / pairs + (pair < a.hi ? 1 : 0);
+  int s = 0, unit;
+  if (i < q) {
+    unit = i * pairs + pair;
   } else {
     s = 1;
     int r = i - q;
-    const int extra = a.lo_tiles - a.hi_tiles, lo_pairs = pairs - a.hi;
+    const int extra = a.lo_units - a.hi_units, lo_pairs = pairs - a.hi;
     if (pair >= a.hi) {
       if (r < extra) {
-        tile = r * lo_pairs + (pair - a.hi);
+        unit = r * lo_pairs + (pair - a.hi);
       } else {
         r -= extra;
-        if (r >= a.hi_tiles) return false;
-        tile = extra * lo_pairs + r * pairs + (pair - a.hi);
+        if (r >= a.hi_units) return false;
+        unit = extra * lo_pairs + r * pairs + (pair - a.hi);
       }
     } else {
-      if (r >= a.hi_tiles) return false;
-      tile = extra * lo_pairs + r * pairs + lo_pairs + pair;
+      if (r >= a.hi_units) return false;
+      unit = extra * lo_pairs + r * pairs + lo_pairs + pair;
     }
-    if (tile >= a.side[1].tiles) return false;
+    if (unit >= a.side[1].tiles * a.side[1].splits) return false;
   }
   const GradSide& g = a.side[s];
+  const int tile = unit / g.splits, part = unit - tile * g.splits;
   const int nt = tile % g.n_nt, mt = tile / g.n_nt;
   u.dw = g.dw;
-  u.splits = a.split ? g.splits : 1;
-  u.kb0 = a.split ? z * g.per_split : 0;
-  u.kb1 = a.split ? min(g.n_kb, u.kb0 + g.per_split) : g.n_kb;
+  u.kb0 = part * g.per_split;
+  u.kb1 = min(g.n_kb, u.kb0 + g.per_split);
+  u.slot = g.splits > 1 ? g.slot0 + unit : -1;
   u.n0 = nt * bn;
   u.z = g.dw ? mt / g.n_mt : 0;
   u.m0 = (g.dw ? mt % g.n_mt : mt) * 256;
@@ -457,68 +451,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     if (a.dbias)  // while the first tile is summed
       for (int c = ((int)blockIdx.x * kGradEpiWarps + ew) * 4; c < 2 * a.F; c += (int)gridDim.x * kGradEpiWarps * 4)
         dbias_columns(a.part, 2 * a.F, a.row_blocks, c, lane, a.dbias);
-    if (a.split && grad_unit(a, pair, pairs, 0, BN, u) && u.splits > 1) {
-      if (mbar_wait_warp(&accf_bar[0], 0, &abort_sh, tmo)) {
-        tc_fence_after();
-        const int r0 = lq * 32, c0 = part * C::WCOLS;
-        const uint32_t taddr = tmem + ((uint32_t)r0 << 16) + (uint32_t)c0;
-        float* mine = a.partial + ((size_t)pair * 256 + (size_t)rank * 128 + r0) * BN + c0;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int i = 0; grad_unit(a, pair, pairs, i, BN, u); ++i) {
+      if (!mbar_wait_warp(&accf_bar[acc], acc_phase, &abort_sh, tmo)) {
+        if (lane == 0) give_up(4);
+        break;
+      }
+      tc_fence_after();
+      const int r0 = (int)rank * 128 + lq * 32, c0 = part * C::WCOLS;
+      const int row0 = u.m0 + r0, col0 = u.n0 + c0;
+      const int rows = min(32, (u.dw ? a.F : a.T) - row0);
+      uint8_t* out = static_cast<uint8_t*>(u.dw ? a.dW : a.dX) +
+                     ((int64_t)(u.dw ? u.z * a.F : 0) + row0) * a.k * 2;
+      float* fp32 = a.partial + ((size_t)max(u.slot, 0) * 256 + r0) * BN + c0;
+      const uint32_t taddr = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * BN + c0);
 #pragma unroll 1
-        for (int c = 0; c < C::WCOLS; c += 32) {
+      for (int c = 0; c < C::WCOLS; c += 64) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           float v[32];
           __syncwarp();
-          tmem_ld32(taddr + (uint32_t)c, *reinterpret_cast<uint32_t(*)[32]>(v));
+          tmem_ld32(taddr + (uint32_t)(c + 32 * h), *reinterpret_cast<uint32_t(*)[32]>(v));
           tmem_wait_ld();
-          stage_row<OUT_F32, 128, 32>(buf, (uint32_t)lane, 0, v);
-          __syncwarp();
-          stage_flush<128, 4>(buf, reinterpret_cast<uint8_t*>(mine + c), (int64_t)BN * 4, 32, 128, true, lane);
-          __syncwarp();
-        }
-      } else if (lane == 0) {
-        give_up(4);
-      }
-    } else {
-      int acc = 0;
-      uint32_t acc_phase = 0;
-      for (int i = 0; grad_unit(a, pair, pairs, i, BN, u); ++i) {
-        if (!mbar_wait_warp(&accf_bar[acc], acc_phase, &abort_sh, tmo)) {
-          if (lane == 0) give_up(4);
-          break;
-        }
-        tc_fence_after();
-        const int row0 = u.m0 + (int)rank * 128 + lq * 32, col0 = u.n0 + part * C::WCOLS;
-        const int rows = min(32, (u.dw ? a.F : a.T) - row0);
-        uint8_t* out = static_cast<uint8_t*>(u.dw ? a.dW : a.dX) +
-                       ((int64_t)(u.dw ? u.z * a.F : 0) + row0) * a.k * 2;
-        const uint32_t taddr = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * BN + part * C::WCOLS);
-#pragma unroll 1
-        for (int c = 0; c < C::WCOLS; c += 64) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t r[32];
+          if (h == 1 && c + 64 == C::WCOLS) {
+            tc_fence_before();
             __syncwarp();
-            tmem_ld32(taddr + (uint32_t)(c + 32 * h), r);
-            tmem_wait_ld();
-            if (h == 1 && c + 64 == C::WCOLS) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster_relaxed(acce_lead0 + 8u * (uint32_t)acc);
-            }
-            float v[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+            if (lane == 0) mbar_arrive_cluster_relaxed(acce_lead0 + 8u * (uint32_t)acc);
+          }
+          if (u.slot >= 0) {
+            stage_row<OUT_F32, 128, 32>(buf, (uint32_t)lane, 0, v);
+            __syncwarp();
+            stage_flush<128, 4>(buf, reinterpret_cast<uint8_t*>(fp32 + c + 32 * h), (int64_t)BN * 4, 32, 128, true, lane);
+          } else {
             stage_row<OT, 128, 32>(buf, (uint32_t)lane, (uint32_t)(4 * h), v);
           }
-          __syncwarp();
-          if (rows > 0 && col0 + c < a.k)
-            stage_flush<128, 2>(buf, out + (int64_t)(col0 + c) * 2, (int64_t)a.k * 2, rows, min(64, a.k - col0 - c) * 2,
-                                true, lane);
-          __syncwarp();
         }
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
+        __syncwarp();
+        if (u.slot < 0 && rows > 0 && col0 + c < a.k)
+          stage_flush<128, 2>(buf, out + (int64_t)(col0 + c) * 2, (int64_t)a.k * 2, rows, min(64, a.k - col0 - c) * 2,
+                              true, lane);
+        __syncwarp();
+      }
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
       }
     }
   }
@@ -543,7 +520,7 @@ __global__ void __launch_bounds__(256) grad_join_kernel(const GradArgs a) {
   const int t0 = a.side[0].splits > 1 ? a.side[0].tiles : 0;  // split tiles of side 0 come first
   const int s = (int)blockIdx.y >= t0 ? 1 : 0, tile = (int)blockIdx.y - s * t0;
   const GradSide& g = a.side[s];
-  const int first = s * a.side[0].tiles * a.side[0].splits + tile * g.splits;
+  const int first = g.slot0 + tile * g.splits;
   const int nt = tile % g.n_nt, mt = tile / g.n_nt, z = g.dw ? mt / g.n_mt : 0;
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), m = (g.dw ? mt % g.n_mt : mt) * 256 + row;
   if (m >= (g.dw ? a.F : a.T)) return;
@@ -574,7 +551,7 @@ cudaError_t launch_grad_t(int grid, const GradMaps& m, const GradArgs& a, cudaSt
   cudaError_t e = smem_opt_in(kern, GradCfg<BN>::SMEM, opted);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3((unsigned)(2 * grid)), kGradThreads, GradCfg<BN>::SMEM, s, 0, m.pw, m.px, m.x, m.w, a);
-  if (e != cudaSuccess || !a.split) return e;
+  if (e != cudaSuccess) return e;
   const int tiles = (a.side[0].splits > 1 ? a.side[0].tiles : 0) + (a.side[1].splits > 1 ? a.side[1].tiles : 0);
   return tiles ? launch_pdl(grad_join_kernel<DT, BN>, dim3(32, (unsigned)tiles), 256, 0, s, 0, a) : cudaSuccess;
 }
@@ -601,12 +578,40 @@ cudaError_t launch_dp(bool vec, const void* P, const void* dY, int T, int F, int
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// The launch for tiles bn columns wide on at most `pairs` CTA pairs.  Unless the
-// sums are split, side 0 (the longer sums) goes round the pairs and side 1 goes on
-// top so that the fullest pair has the least to do.  Returns that pair's stages
-// (with a fixed part per tile), -1 when there are too many tiles.
-int64_t plan_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw, int bn, int pairs, GradArgs* a, int* grid) {
-  constexpr int kFixed = 6;  // a tile's fill and drain, in stages
+// Shares the units of two products out over at most `pairs` CTA pairs: side 0 (the
+// longer units) goes round the pairs, side 1 on top so that the fullest pair has
+// the least to do.  Returns that pair's stages, with a fixed part per unit.
+int64_t share_out(const GradSide& x, const GradSide& y, int pairs, GradArgs* a, int* grid) {
+  constexpr int kFixed = 6;  // a unit's fill and drain, in stages
+  const bool x_first = x.per_split >= y.per_split;
+  a->side[0] = x_first ? x : y;
+  a->side[1] = x_first ? y : x;
+  const int64_t n0 = (int64_t)a->side[0].tiles * a->side[0].splits, n1 = (int64_t)a->side[1].tiles * a->side[1].splits;
+  const int64_t c0 = a->side[0].per_split + kFixed, c1 = a->side[1].per_split + kFixed;
+  *grid = (int)std::min<int64_t>(n0 + n1, pairs);
+  const int64_t q = n0 / *grid;
+  a->hi = (int)(n0 % *grid);
+  // the lowest level (in stages) at which every unit of side 1 finds room
+  auto room = [&](int64_t level, int64_t* lo, int64_t* hi) {
+    *lo = std::max<int64_t>(0, (level - q * c0) / c1);
+    *hi = a->hi ? std::max<int64_t>(0, (level - (q + 1) * c0) / c1) : *lo;
+    return *lo * (*grid - a->hi) + *hi * a->hi >= n1;
+  };
+  int64_t lo = 0, hi = 0, below = (n0 * c0 + n1 * c1) / *grid - 1, level = below + c0 + c1 + 1;
+  while (level - below > 1) {  // room at `level` (the average and a unit of each side more), none at `below`
+    const int64_t mid = (below + level) / 2;
+    (room(mid, &lo, &hi) ? level : below) = mid;
+  }
+  room(level, &lo, &hi);
+  a->lo_units = (int)lo;
+  a->hi_units = (int)hi;
+  return std::max(q * c0 + lo * c1, a->hi ? (q + 1) * c0 + hi * c1 : 0);
+}
+
+// The launch for tiles bn columns wide: its stages (share_out), or -1 when there
+// are too many tiles.
+int64_t plan_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw, int bn, int pairs, bool may_cut, GradArgs* a,
+                  int* grid) {
   const int64_t F = h->n_out / 2;
   const int n_nt = (int)((h->k + bn - 1) / bn);
   a->F = (int)F;
@@ -625,60 +630,45 @@ int64_t plan_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw, int
   sw.tiles = (int)w_tiles;
   sx.tiles = (int)x_tiles;
   sw.splits = sx.splits = 1;
-  const bool w_first = sw.n_kb >= sx.n_kb;
-  a->side[0] = w_first ? sw : sx;
-  a->side[1] = w_first ? sx : sw;
-  *grid = (int)std::min<int64_t>(w_tiles + x_tiles, pairs);
-  const int64_t c0 = a->side[0].n_kb + kFixed, c1 = a->side[1].n_kb + kFixed;
-  const int64_t q = a->side[0].tiles / *grid;
-  a->hi = a->side[0].tiles % *grid;
-  int64_t lo = 0, hi = 0;
-  for (int64_t level = (a->side[1].tiles * c1 + a->side[0].tiles * c0) / *grid;; level += c1 / 8 + 1) {
-    lo = std::max<int64_t>(0, (level - q * c0) / c1);
-    hi = a->hi ? std::max<int64_t>(0, (level - (q + 1) * c0) / c1) : lo;
-    if (lo * (*grid - a->hi) + hi * a->hi >= a->side[1].tiles) break;
-  }
-  a->lo_tiles = (int)lo;
-  a->hi_tiles = (int)hi;
-  int64_t cost = std::max(q * c0 + lo * c1, a->hi ? (q + 1) * c0 + hi * c1 : 0);
-  if (w_tiles + x_tiles >= pairs) return cost;
+  sw.per_split = sw.n_kb;
+  sx.per_split = sx.n_kb;
+  int64_t cost = share_out(sw, sx, pairs, a, grid);
+  if (!may_cut) return cost;
 
-  // Fewer tiles than pairs: cut the sums into parts of at most `len` stages, one
-  // part per pair.  Joining them (fp32 tiles out to L2, another launch) costs about
-  // kJoin stages.
+  // Cut long sums into parts of at most `len` stages where that leaves the fullest
+  // pair less to do.  Joining the parts (fp32 tiles out to L2, another launch)
+  // costs about kJoin stages.  The workspace holds a partial tile per pair.
   constexpr int kJoin = 24;
-  const char* whole = getenv("NMSPMM_GRAD_SPLIT");  // 0: no split (tests and sweeps)
-  if (whole && whole[0] == '0') return cost;
-  for (int len = 8; len < a->side[0].n_kb || len < a->side[1].n_kb; len += len / 4) {
-    int64_t units = 0;
-    int split[2], per[2];
-    for (int i = 0; i < 2; ++i) {
-      const int n = a->side[i].n_kb;
-      split[i] = (n + len - 1) / len;
-      per[i] = (n + split[i] - 1) / split[i];
-      split[i] = (n + per[i] - 1) / per[i];  // no part is empty
-      units += (int64_t)a->side[i].tiles * split[i];
+  const int longest = std::max(sw.tiles ? sw.n_kb : 0, sx.tiles ? sx.n_kb : 0);
+  const int64_t sum = (int64_t)sw.tiles * sw.n_kb + (int64_t)sx.tiles * sx.n_kb;
+  for (int len = 8; len < longest && std::max<int64_t>(len, sum / pairs) + kJoin < cost; len += len / 2) {
+    GradSide side[2] = {sw, sx};
+    int64_t parts = 0;
+    for (GradSide& g : side) {
+      g.splits = g.tiles ? (g.n_kb + len - 1) / len : 1;
+      g.per_split = (g.n_kb + g.splits - 1) / g.splits;
+      g.splits = (g.n_kb + g.per_split - 1) / g.per_split;  // no part is empty
+      g.slot0 = (int)parts;
+      if (g.splits > 1) parts += (int64_t)g.tiles * g.splits;
+      if (parts > pairs) break;
     }
-    if (units > pairs) continue;
-    const int64_t c = len + kFixed + kJoin;
-    if (c < cost) {
-      cost = c;
-      a->split = 1;
-      *grid = (int)units;
-      for (int i = 0; i < 2; ++i) {
-        a->side[i].splits = split[i];
-        a->side[i].per_split = per[i];
-      }
+    if (parts > pairs || parts == 0) continue;
+    GradArgs c = *a;
+    int g = 0;
+    const int64_t level = share_out(side[0], side[1], pairs, &c, &g) + kJoin;
+    if (level < cost) {
+      cost = level;
+      *a = c;
+      *grid = g;
     }
   }
   return cost;
 }
 
-// Workspace: dp, the masked dense weight, the row blocks' column sums, and for
-// split launches their partial tiles (a unit per pair at most).
+// Workspace: dp, the masked dense weight, the row blocks' column sums, and partial
+// tiles of cut sums (one per pair at most).
 struct GradWs {
   int64_t pitch, dp, wm, part, partial, total;
-  bool may_split;
   GradWs(const nm_handle* h, int64_t T) {
     const int64_t F = h->n_out / 2, pairs = num_sms(h->device) / 2;
     pitch = (F + 63) / 64 * 64;  // whole 128-byte lines: a 128-byte box row then touches one
@@ -687,10 +677,9 @@ struct GradWs {
     part = wm + align256(h->n_out * h->k * 2);
     const int64_t rows = dp_block_rows(T, F);
     partial = part + align256((T + rows - 1) / rows * h->n_out * 4);
-    // a 128-wide tiling with as many tiles as pairs is not split, nor is any wider one then
+    // with more 128-wide tiles than twice the pairs on both sides nothing is cut
     const int64_t n_nt = (h->k + 127) / 128, tiles = std::min(2 * ((F + 255) / 256), (T + 255) / 256) * n_nt;
-    may_split = tiles < 2 * pairs;
-    total = partial + (may_split ? pairs * 256 * 256 * 4 : 0);
+    total = partial + (tiles <= 2 * pairs ? pairs * 256 * 256 * 4 : 0);
   }
 };
 
@@ -703,15 +692,39 @@ int forced_grad_bn() {  // tests and sweeps
 // launch.  A stage of a 256-wide tile takes 1.45 times a 128-wide one's (0.33
 // against 0.23 us over full waves, 0.28 against 0.19 when few tiles run; the
 // narrower tile moves 24 KB a stage and SM against 32 KB for half the products).
+// The choice is a function of the shape alone; a thread's last one is kept, since a
+// training step asks for the same again and again.
 nm_status choose_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw, GradArgs* a, int* grid, int* bn) {
+  struct Key {
+    int64_t n_out, k, T;
+    int want, pairs, forced, whole;
+    bool operator==(const Key& o) const {
+      return n_out == o.n_out && k == o.k && T == o.T && want == o.want && pairs == o.pairs && forced == o.forced &&
+             whole == o.whole;
+    }
+  };
+  struct Choice {
+    Key key{};
+    GradArgs a{};
+    int grid = 0, bn = 0;
+  };
+  static thread_local Choice last;
   const int pairs = num_sms(h->device) / 2, forced = forced_grad_bn();
+  const char* split = getenv("NMSPMM_GRAD_SPLIT");  // 0: no split (tests and sweeps)
+  const Key key{h->n_out, h->k, T, (want_dx ? 1 : 0) + (want_dw ? 2 : 0), pairs, forced, split && split[0] == '0'};
+  if (last.bn && last.key == key) {
+    *a = last.a;
+    *grid = last.grid;
+    *bn = last.bn;
+    return NM_OK;
+  }
   *bn = 0;
   double best = 1e300;
   for (int w : {256, 128}) {
     if (forced && w != forced) continue;
     GradArgs c{};
     int g = 0;
-    const int64_t level = plan_grad(h, T, want_dx, want_dw, w, pairs, &c, &g);
+    const int64_t level = plan_grad(h, T, want_dx, want_dw, w, pairs, !key.whole, &c, &g);
     if (level < 0) return fail(NM_ERR_UNSUPPORTED, "T x k too large");
     const double cost = (double)level * (w == 256 ? 1.45 : 1.0);
     if (cost < best) {
@@ -721,7 +734,12 @@ nm_status choose_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw,
       *grid = g;
     }
   }
-  return *bn ? NM_OK : fail(NM_ERR_INVALID, "NMSPMM_FORCE_GRAD_BN must be 128 or 256");
+  if (!*bn) return fail(NM_ERR_INVALID, "NMSPMM_FORCE_GRAD_BN must be 128 or 256");
+  last.key = key;
+  last.a = *a;
+  last.grid = *grid;
+  last.bn = *bn;
+  return NM_OK;
 }
 
 nm_status check_grad(const nm_handle* h, int64_t T) {
@@ -816,7 +834,8 @@ nm_status nm_gated_backward(const nm_handle* h, const void* X, const void* P, co
   GradArgs a{};
   int bn = 0, grid = 0;
   if ((dX || dW) && (st = choose_grad(h, T, dX != nullptr, dW != nullptr, &a, &grid, &bn)) != NM_OK) return st;
-  if (a.split && !lay.may_split) return fail(NM_ERR_INVALID, "the workspace has no room for a split launch");
+  if ((a.side[0].splits > 1 || a.side[1].splits > 1) && lay.partial == lay.total)
+    return fail(NM_ERR_INVALID, "the workspace has no room for partial tiles");
   cudaError_t e = cudaSuccess;
   const bool vec = F % 8 == 0;  // every row starts on 16 bytes
   e = h->dt == DT_F16 ? launch_dp<DT_F16>(vec, P, dY, (int)T, (int)F, (int)lay.pitch, (int)act, dp, part, un, s)
