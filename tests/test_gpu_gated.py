@@ -401,6 +401,70 @@ def test_two_streams_share_a_handle():
             assert torch.equal(a[0], c[0]) and torch.equal(a[1], c[1])
 
 
+def test_far_rows_match_a_small_call(monkeypatch):
+    """Element offsets past 2^31 in p and dp."""
+    monkeypatch.setenv("NMSPMM_GRAD_SPLIT", "0")     # the same order of sums in both calls
+    T, k, F, tail = 140_011, 64, 8192, 130
+    g = torch.Generator(device="cuda").manual_seed(1)
+    X = torch.randn((T, k), generator=g, device="cuda").bfloat16()
+    W = torch.randn((2 * F, k), generator=g, device="cuda").bfloat16()
+    h = nm.nm_compress_gated(W, 2, 4)
+    P = torch.empty((T, 2 * F), dtype=torch.bfloat16, device="cuda")
+    Y = nm.nm_spmm_gated(h, X, P=P)
+    p = torch.empty((tail, 2 * F), dtype=torch.bfloat16, device="cuda")
+    y = nm.nm_spmm_gated(h, X[-tail:].contiguous(), P=p)
+    # the two calls' plans differ (token tiles, cluster splits), so their sums may, by the
+    # bound of the header on either side; then a step of bf16 (2^-7) apart, and for
+    # y = silu(g) u what those differences make of it (|silu'| < 1.1, |silu(g)| <= |g|)
+    e = 2 * (k / 8 + 4) * 2.0 ** -23 * (X[-tail:].float().abs() @ W.float().abs().t())
+    gate, up = p[:, :F].float().abs(), p[:, F:].float().abs()
+    assert bool(((P[-tail:].float() - p.float()).abs() <= e + 2.0 ** -7 * (p.float().abs() + e)).all())
+    ey = 1.1 * e[:, :F] * (1.01 * up + e[:, F:]) + (1.01 * gate + e[:, :F]) * e[:, F:]
+    assert bool(((Y[-tail:].float() - y.float()).abs() <= ey + 2.0 ** -7 * (y.float().abs() + ey)).all())
+    dX, dW, db = nm.nm_gated_backward(h, X, P, Y, bias_grad=True)
+    small = nm.nm_gated_backward(h, X[-tail:].contiguous(), P[-tail:].contiguous(), Y[-tail:].contiguous())
+    assert torch.equal(dX[-tail:], small[0])
+    # dW and dbias are sums over T: halves of the batch add up to the whole
+    half = 70_016
+    parts = [nm.nm_gated_backward(h, X[r].contiguous(), P[r].contiguous(), Y[r].contiguous(), bias_grad=True)
+             for r in (slice(0, half), slice(half, T))]
+    for i, whole in ((1, dW), (2, db)):
+        a, b = parts[0][i].double(), parts[1][i].double()
+        assert float((a + b - whole.double()).norm() / whole.double().norm()) < (1e-2 if i == 1 else 1e-5)
+
+
+def test_host_threads_share_a_handle():
+    import threading
+    W = torch.randn((512, 256), device="cuda").bfloat16()
+    h = nm.nm_compress_gated(W, 2, 4)
+    xs = [torch.randn((t, 256), device="cuda").bfloat16() for t in (20, 300, 1500)]
+
+    def block(x):
+        p = torch.empty((x.shape[0], 512), dtype=torch.bfloat16, device="cuda")
+        y = nm.nm_spmm_gated(h, x, P=p)
+        return (y, p) + nm.nm_gated_backward(h, x, p, y, bias_grad=True)
+
+    want = [block(x) for x in xs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(30):
+                got = block(xs[i])
+                s.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
 def test_refusals_on_a_handle(monkeypatch):
     W8 = torch.randint(-127, 128, (64, 64), dtype=torch.int8).cuda()
     h8, plain = nm.nm_compress_gated(W8, 2, 4), nm.nm_compress(W8, 2, 4)

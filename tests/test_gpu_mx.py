@@ -150,12 +150,53 @@ def test_dequantise_every_code_and_scale():
     np.testing.assert_array_equal(f64(nm.nm_mx_dequantize(Q, S, dtype=torch.float16)), f64(got.to(torch.float16)))
 
 
-def test_quantise_large_matches_itself_in_slices():
-    """Offsets past 2^31 elements would show as rows that differ from a small call's."""
-    x = torch.randn((70001, 512), device="cuda").to(torch.bfloat16)
+def test_far_rows_match_a_small_call():
+    """Element offsets past 2^31 in the activation, its codes' values and the output."""
+    T, k, n, tail = 4_300_033, 512, 512, 161
+    x = torch.empty((T, k), dtype=torch.bfloat16, device="cuda")
+    x[-tail:].normal_()
+    x[:-tail] = x[-tail]
+    start = (T - tail) // 128 * 128             # the small call's rows start on a scale tile
+    small = x[start:].clone()
     Q, S = nm.nm_mx_quantize(x)
-    q, s = nm.nm_mx_quantize(x[69888:].contiguous())
-    assert torch.equal(Q[69888:], q) and torch.equal(S.view(-1, 2048)[546:].reshape(-1), s)
+    q, s = nm.nm_mx_quantize(small)
+    assert torch.equal(Q[start:], q) and torch.equal(S.view(-1, 2048)[start // 128:].reshape(-1), s)
+    nm.nm_mx_dequantize(Q, S, X=x)
+    assert torch.equal(x[start:], nm.nm_mx_dequantize(q, s))
+    W = make(n, k, torch.bfloat16, 3).cuda()
+    h = nm.nm_compress_mx(W)
+    Y = nm.nm_spmm_mx(h, Q, S, Y=x)             # the values are not needed any more
+    assert torch.equal(Y[start:], nm.nm_spmm_mx(h, q, s))
+    assert torch.equal(Y[0], Y[1_000_000])      # equal rows in, equal rows out
+    hg = nm.nm_compress_mx(W, gated=True)
+    Yg = nm.nm_spmm_mx_gated(hg, Q, S, out="float32")
+    assert torch.equal(Yg[start:], nm.nm_spmm_mx_gated(hg, q, s, out="float32"))
+
+
+def test_host_threads_share_a_handle():
+    import threading
+    W = make(512, 512, torch.bfloat16, 5).cuda()
+    h = nm.nm_compress_mx(W)
+    xs = [make(t, 512, torch.bfloat16, 6 + t).cuda() for t in (33, 700, 1300)]
+    want = [nm.nm_spmm_mx(h, *nm.nm_mx_quantize(x)) for x in xs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(50):
+                y = nm.nm_spmm_mx(h, *nm.nm_mx_quantize(xs[i]))
+                s.synchronize()
+                if not torch.equal(y, want[i]):
+                    bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
 
 
 @pytest.mark.parametrize("N,M", [(1, 4), (2, 4), (2, 8), (4, 8), (4, 4), (8, 8)])
