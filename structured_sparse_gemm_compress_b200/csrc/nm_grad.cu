@@ -50,7 +50,7 @@ template <int DT, bool VEC>
 __device__ __forceinline__ void dp_load(const uint16_t* row, int f0, int F, int lane, float (&v)[8]) {
   if constexpr (VEC) {
     uint4 q = make_uint4(0u, 0u, 0u, 0u);
-    if (f0 + lane * 8 < F) q = __ldg(reinterpret_cast<const uint4*>(row + f0 + lane * 8));
+    if (f0 + lane * 8 < F) q = __ldcs(reinterpret_cast<const uint4*>(row + f0 + lane * 8));  // read once: leave L2 to dp
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
