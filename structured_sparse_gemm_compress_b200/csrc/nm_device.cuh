@@ -541,6 +541,25 @@ __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// 16 lanes x 16 consecutive 32-bit columns, spread over the warp's 32 threads as
+// fragments: of each 8 columns, thread t gets lane t / 4 (r[0], r[1]) and lane
+// t / 4 + 8 (r[2], r[3]) at columns 2 (t % 4) and one more.  taddr names lane 0 or
+// lane 16 of the warp's quarter.
+__device__ __forceinline__ void tmem_ld16l_x16(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+// Four 8 x 8 matrices of 16-bit elements to shared memory, transposed: thread t
+// holds elements (t / 4, 2 (t % 4)) and (.., + 1) of each, and gives the address of
+// row t % 8 (8 elements, 16 bytes) of the transposed matrix t / 8.
+__device__ __forceinline__ void stmatrix_x4_trans(void* row, uint32_t m0, uint32_t m1, uint32_t m2, uint32_t m3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(row)), "r"(m0),
+               "r"(m1), "r"(m2), "r"(m3)
+               : "memory");
+}
+
 // 32 lanes x 8 consecutive 32-bit columns.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"

@@ -438,15 +438,9 @@ __device__ __forceinline__ void gate_store(const SpmmArgs& a, const float (&y)[H
 }
 
 // One warp's run of CH tokens starting at token t0; row: this lane's packed row.
-// STAGED: p leaves by way of pbuf (kOutSave), shared by the four warps `part` of
-// the tile's lane quarters: [CH tokens][gate, up][64 channels], the 16-byte pieces
-// of the up half rotated by 64 bytes so that a warp's gate and up lanes write
-// different banks.  Directly, each of a warp's stores of p covers two 32-byte
-// runs, and saving p took 30 us of an 87 us launch (6304 x 1024 -> 2 x 4096);
-// gathered, a store covers four whole lines.
-template <int DT, int CH, bool STAGED = false>
+template <int DT, int CH>
 __device__ __forceinline__ void gate_run(const SpmmArgs& a, const EpiCh& e, const uint32_t (&r)[CH], int row, int t0,
-                                         int lane, uint8_t* pbuf = nullptr, int part = 0) {
+                                         int lane) {
   constexpr int H = CH / 2;
   float f[CH];
 #pragma unroll
@@ -464,12 +458,7 @@ __device__ __forceinline__ void gate_run(const SpmmArgs& a, const EpiCh& e, cons
   const int ch = (row >> 5) * 16 + (row & 15);
   const bool ch_ok = ch < a.n_ff;
   const bool up = (lane & 16) != 0;
-  if constexpr (STAGED) {
-    const uint32_t c = (uint32_t)(ch & 63) * 2u;  // byte of the channel within the tile's half row
-    uint8_t* dst = pbuf + (up ? 128u : 0u) + (c ^ (up ? 64u : 0u));
-#pragma unroll
-    for (int j = 0; j < CH; ++j) gate_save<DT>(dst + j * 256, 0, f[j]);
-  } else if constexpr (DT != DT_I8) {
+  if constexpr (DT != DT_I8) {
     if (a.P && ch_ok) {
       const size_t base = (size_t)t0 * (2 * (size_t)a.n_ff) + (size_t)(up ? a.n_ff + ch : ch);
 #pragma unroll
@@ -498,17 +487,155 @@ __device__ __forceinline__ void gate_run(const SpmmArgs& a, const EpiCh& e, cons
       default: gate_store<OUT_F32, H>(a, g, base, a.T - ty); break;
     }
   }
-  if constexpr (STAGED) {
-    named_bar_sync(1 + part, 128);  // all four lane quarters' p of these tokens are in pbuf
-    const int tid = ((row >> 5) & 3) * 32 + lane, ch0 = (row >> 7) * 64;
+}
+
+// ---- gated output stage of the two-SM kernel
+//
+// The accumulator's gate and up lanes are read as fragments (tcgen05.ld 16x256b), 16
+// lanes at a time, so that a thread gets the same two channels and four tokens of
+// both: no exchange between lanes.  16-bit values go to shared memory through
+// transposing 8 x 8 matrix stores, token by token, and leave in whole lines of 64
+// channels that the four warps (lane quarters) of a part fill together; one named
+// barrier per 16 tokens, two buffers.  6304 x 1024 -> 2 x 4096 bf16: see nm_gated.cu.
+constexpr int kGateTok = 16;            // tokens of one step
+constexpr int kGateY = kGateTok * 128;  // staged Y bytes (64 channels of 16 bits; INT8 uses half)
+constexpr int kGateP = kGateTok * 256;  // staged p bytes: [token][gate, up][64 channels]
+
+struct GateCh {  // a thread's two channels c and c + 8
+  float sg[2], su[2], bg[2], bu[2];
+  __device__ __forceinline__ void fetch(const SpmmArgs& a, int c) {
 #pragma unroll
-    for (int i = 0; i < CH / 8; ++i) {
-      const int piece = tid + 128 * i, t = t0 + piece / 16, z = (piece >> 3) & 1, c = piece & 7;
-      if (t < a.T && ch0 + c * 8 < a.n_ff) {
-        const uint4 q = *reinterpret_cast<const uint4*>(pbuf + (piece / 16) * 256 + z * 128 + ((c * 16) ^ (z * 64)));
-        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.P) + (size_t)t * (2 * (size_t)a.n_ff) +
-                                  (size_t)z * a.n_ff + ch0 + c * 8) = q;
+    for (int i = 0; i < 2; ++i) {
+      const bool in = c + 8 * i < a.n_ff;
+      sg[i] = a.scale && in ? __ldg(a.scale + c + 8 * i) : 1.0f;
+      su[i] = a.scale && in ? __ldg(a.scale + a.n_ff + c + 8 * i) : 1.0f;
+      bg[i] = a.bias && in ? __ldg(a.bias + c + 8 * i) : 0.0f;
+      bu[i] = a.bias && in ? __ldg(a.bias + a.n_ff + c + 8 * i) : 0.0f;
+    }
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ void gate_values(const SpmmArgs& a, const uint32_t (&r)[8], const float (&s)[2],
+                                            const float (&b)[2], float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = DT == DT_I8 ? __int2float_rn((int32_t)r[j]) : __uint_as_float(r[j]);
+  if (a.scale) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const float f = s[(j >> 1) & 1];
+      upk2(mul2(pk2(v[j], v[j + 1]), pk2(f, f)), v[j], v[j + 1]);
+    }
+  }
+  if (a.bias) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const float f = b[(j >> 1) & 1];
+      upk2(add2(pk2(v[j], v[j + 1]), pk2(f, f)), v[j], v[j + 1]);
+    }
+  }
+}
+
+template <int OT>
+__device__ __forceinline__ uint32_t pack16_pair(float x, float y) {
+  if constexpr (OT == OUT_F16) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+// Eight values (two channels x 16 tokens of the warp, by fragment) into a staged
+// [token][64 channels] half row; row: this lane's matrix row address.
+template <int OT>
+__device__ __forceinline__ void gate_stage(uint8_t* row, const float (&v)[8]) {
+  stmatrix_x4_trans(row, pack16_pair<OT>(v[0], v[1]), pack16_pair<OT>(v[2], v[3]), pack16_pair<OT>(v[4], v[5]),
+                    pack16_pair<OT>(v[6], v[7]));
+}
+// `n` of the 16 / sizeof(T) elements at src to dst, at once when they may be.
+template <typename T>
+__device__ __forceinline__ void gate_piece(T* dst, const uint8_t* src, int n, bool vec) {
+  if (vec) {
+    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+  } else {
+    for (int i = 0; i < min(n, 16 / (int)sizeof(T)); ++i) dst[i] = reinterpret_cast<const T*>(src)[i];
+  }
+}
+
+// One warp's step: 16 tokens from t0 of its lane quarter's 16 channels (tile ct).
+template <int DT, bool SAVE>
+__device__ __forceinline__ void gate_step(const SpmmArgs& a, const GateCh& e, const uint32_t (&rg)[8],
+                                          const uint32_t (&ru)[8], int ct, int lq, int t0, int lane, uint8_t* ybuf,
+                                          int part) {
+  float g[8], u[8];
+  gate_values<DT>(a, rg, e.sg, e.bg, g);
+  gate_values<DT>(a, ru, e.su, e.bu, u);
+  const int ch = ct * (kRows / 2) + lq * 16 + (lane >> 2);  // and ch + 8
+  const int tq = t0 + 2 * (lane & 3);                       // tokens of v[0], v[1]; v[4], v[5]: 8 more
+  // this lane's row of the staged matrices: token, and which 8 of the quarter's 16
+  // channels; 16-byte pieces of a row are permuted by its token, against bank conflicts
+  const int tok = ((lane >> 4) << 3) + (lane & 7);
+  const uint32_t piece = (uint32_t)((lq * 2 + ((lane >> 3) & 1)) ^ (tok & 7)) << 4;
+  uint8_t* pbuf = ybuf + kGateY;
+  if constexpr (SAVE) {
+    constexpr int OT = DT == DT_F16 ? OUT_F16 : OUT_BF16;
+    gate_stage<OT>(pbuf + tok * 256 + piece, g);
+    gate_stage<OT>(pbuf + tok * 256 + 128 + piece, u);
+  } else if constexpr (DT != DT_I8) {
+    if (a.P) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = ch + ((j & 2) ? 8 : 0), t = tq + (j & 1) + ((j & 4) ? 8 : 0);
+        if (c < a.n_ff && t < a.T) {
+          const size_t at = (size_t)t * (2 * (size_t)a.n_ff) + c;
+          gate_save<DT>(a.P, at, g[j]);
+          gate_save<DT>(a.P, at + a.n_ff, u[j]);
+        }
       }
+    }
+  }
+  act_run<8>(g, a.act);
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) upk2(mul2(pk2(g[j], g[j + 1]), pk2(u[j], u[j + 1])), g[j], g[j + 1]);
+  if (a.out_ty == OUT_F16) {
+    gate_stage<OUT_F16>(ybuf + tok * 128 + piece, g);
+  } else if (a.out_ty == OUT_BF16) {
+    gate_stage<OUT_BF16>(ybuf + tok * 128 + piece, g);
+  } else if (a.out_ty == OUT_I8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = lq * 16 + (lane >> 2) + ((j & 2) ? 8 : 0), t = 2 * (lane & 3) + (j & 1) + ((j & 4) ? 8 : 0);
+      ybuf[t * 64 + c] = (uint8_t)(int8_t)rne_sat_s8(__fmul_rn(g[j], a.out_scale));
+    }
+  } else {  // fp32: a store covers 8 channels (32 bytes) of 4 tokens
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = ch + ((j & 2) ? 8 : 0), t = tq + (j & 1) + ((j & 4) ? 8 : 0);
+      if (c < a.n_ff && t < a.T) reinterpret_cast<float*>(a.Y)[(size_t)t * a.n_ff + c] = g[j];
+    }
+  }
+  named_bar_sync(1 + part, 128);  // all four lane quarters' values of these tokens are staged
+  const int tid = lq * 32 + lane, c0 = ct * (kRows / 2);
+  if (a.out_ty == OUT_F16 || a.out_ty == OUT_BF16) {
+    const int y = tid >> 3, c = c0 + (tid & 7) * 8, t = t0 + y;
+    if (t < a.T && c < a.n_ff)
+      gate_piece(reinterpret_cast<uint16_t*>(a.Y) + (size_t)t * a.n_ff + c,
+                 ybuf + y * 128 + (((tid & 7) ^ (y & 7)) << 4), a.n_ff - c, a.n_ff % 8 == 0);
+  } else if (a.out_ty == OUT_I8) {
+    const int y = tid >> 2, c = c0 + (tid & 3) * 16, t = t0 + y;
+    if (tid < 64 && t < a.T && c < a.n_ff)
+      gate_piece(reinterpret_cast<uint8_t*>(a.Y) + (size_t)t * a.n_ff + c, ybuf + y * 64 + (tid & 3) * 16, a.n_ff - c,
+                 a.n_ff % 16 == 0);
+  }
+  if constexpr (SAVE) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int n = tid + 128 * i, y = n >> 4, z = (n >> 3) & 1, c = c0 + (n & 7) * 8, t = t0 + y;
+      if (t < a.T && c < a.n_ff)
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.P) + (size_t)t * (2 * (size_t)a.n_ff) +
+                                  (size_t)z * a.n_ff + c) =
+            *reinterpret_cast<const uint4*>(pbuf + y * 256 + z * 128 + (((n & 7) ^ (y & 7)) << 4));
     }
   }
 }
@@ -1312,10 +1439,10 @@ struct PairCfg {
   static constexpr int OES = out_bytes(OUT);
   static constexpr int EPI_BUF = CH * 32 * OES;
   static constexpr int EPI_NB = (kSmemBudget - 2 * EPI_WARPS * EPI_BUF) / STAGE >= 4 ? 2 : 1;
-  // kOutSave: two buffers of CH tokens x 128 packed rows for each group of four warps
-  static constexpr int SAVE_BUF = CH * 256;
-  static constexpr int EPI_BYTES = TS ? EPI_NB * EPI_WARPS * EPI_BUF : (OUT & kOutSave) ? EPI_WARPS / 4 * 2 * SAVE_BUF : 0;
-  static constexpr int STAGES_FIT = (kSmemBudget - EPI_BYTES) / STAGE;
+  // gated: two staging buffers for each group of four warps
+  static constexpr int GATE_BUF = kGateY + ((OUT & kOutSave) ? kGateP : 0);
+  static constexpr int EPI_BYTES = TS ? EPI_NB * EPI_WARPS * EPI_BUF : (OUT & kOutGate) ? EPI_WARPS / 4 * 2 * GATE_BUF : 0;
+  static constexpr int STAGES_FIT = (kSmemBudget - EPI_BYTES - ((OUT & kOutGate) ? 512 : 0)) / STAGE;  // (static: barriers, flags)
   static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
   static constexpr int SMEM = STAGES * STAGE + EPI_BYTES + 1024;
   static_assert(STAGE % 1024 == 0 && B_BOX % 1024 == 0, "stages keep 1024-byte alignment");
@@ -1323,6 +1450,7 @@ struct PairCfg {
   static_assert(COLS_NEEDED <= 512, "tensor memory overflow");
   static_assert(BN % 32 == 0 && BN <= 256, "pair MMA N");
   static_assert(WCOLS % CH == 0, "epilogue chunking");
+  static_assert((OUT & kOutGate) == 0 || WCOLS % kGateTok == 0, "gated steps");
 };
 
 template <int DT, int IMG, int BN, int OUT>
@@ -1349,7 +1477,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(cta_threads(OUT), 1)
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_sh;
-  __shared__ volatile int part_ok_sh[SAVE ? C::EPI_WARPS / 4 : 1][2];
+  __shared__ volatile int part_ok_sh[GATE ? C::EPI_WARPS / 4 : 1][2];
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -1561,12 +1689,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(cta_threads(OUT), 1)
     const int part = ew >> 2;
     uint8_t* stage_buf = smem + (size_t)C::STAGES * C::STAGE + (size_t)ew * C::EPI_NB * C::EPI_BUF;
     int buf = 0, acc = 0, iter = 0;
-    [[maybe_unused]] int pchunk = 0;  // kOutSave: chunks staged so far
+    [[maybe_unused]] int step = 0;  // gated: steps staged so far
     uint32_t acc_phase = 0;
     for (int u = u_first; u < a.units; u += u_step, ++iter) {
       const int pt = u % n_pct, tt = u / n_pct;
       const int ct = 2 * pt + (int)rank;
-      if constexpr (SAVE) {
+      if constexpr (GATE) {
         // The four warps of a part meet at named barriers below: one of them waits
         // and all take the same branch (the flag alternates between two slots).
         if ((ew & 3) == 0) {
@@ -1587,72 +1715,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(cta_threads(OUT), 1)
       }
       if (ep_tid == 0) NM_TR(TR_E_START, iter);
       tc_fence_after();
-      const int ch0 = ct * kRows + lq * 32;
-      const int ch = ch0 + lane;
-      // this lane's row of W (gated: interleaved packed rows)
-      const int wrow = GATE ? (int)gated_source_row(ch, a.n_ff) : ch;
-      const bool ch_ok = GATE ? wrow >= 0 : ch < a.n_out;
-      const bool has_scale = a.scale != nullptr;
-      const float s = (has_scale && ch_ok) ? __ldg(a.scale + wrow) : 1.0f;
-      const float bch = (EPI && a.bias && ch_ok) ? __ldg(a.bias + wrow) : 0.0f;
       const int col0 = part * C::WCOLS;
       const int t0 = tt * BN + col0;
       const uint32_t tbase = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * BN + col0);
+      if constexpr (GATE) {
+        GateCh e;
+        e.fetch(a, ct * (kRows / 2) + lq * 16 + (lane >> 2));
 #pragma unroll 1
-      for (int c = 0; c < C::NCH; ++c) {
-        uint32_t r[C::CH];
-        __syncwarp();  // tcgen05.ld is .sync.aligned: reconverge after the previous chunk's stores
-        tmem_ld_n<C::CH>(tbase + (uint32_t)(c * C::CH), r);
-        tmem_wait_ld();
-        if (c == C::NCH - 1) {  // release the accumulator (the peer's release is forwarded by its warp 1)
-          tc_fence_before();
+        for (int c = 0; c < C::WCOLS; c += kGateTok, ++step) {
+          uint32_t rg[8], ru[8];
           __syncwarp();
-          if (lane == 0) {
-            if (leader)
-              mbar_arrive(&acce_bar[acc]);
-            else if constexpr (C::TS)
-              mbar_arrive_cluster(acce_lead0 + 8u * (uint32_t)acc);
-            else
-              mbar_arrive(&pfree_bar[acc]);
+          tmem_ld16l_x16(tbase + (uint32_t)c, rg);
+          tmem_ld16l_x16(tbase + (16u << 16) + (uint32_t)c, ru);
+          tmem_wait_ld();
+          if (c + kGateTok == C::WCOLS) {  // release the accumulator (the peer's release is forwarded by its warp 1)
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(leader ? &acce_bar[acc] : &pfree_bar[acc]);
           }
+          uint8_t* ybuf = smem + (size_t)C::STAGES * C::STAGE + (size_t)(2 * part + (step & 1)) * C::GATE_BUF;
+          gate_step<DT, SAVE>(a, e, rg, ru, ct, lq, t0 + c, lane, ybuf, part);
         }
-        const int tc0 = t0 + c * C::CH;
-        if (C::TS && a.tma_store) {
-          if (lane == 0) {
-            if (C::EPI_NB == 2) bulk_wait_read<1>(); else bulk_wait_read<0>();
+      } else {
+        const int ch0 = ct * kRows + lq * 32;
+        const int ch = ch0 + lane;
+        const bool ch_ok = ch < a.n_out;
+        const bool has_scale = a.scale != nullptr;
+        const float s = (has_scale && ch_ok) ? __ldg(a.scale + ch) : 1.0f;
+        const float bch = (EPI && a.bias && ch_ok) ? __ldg(a.bias + ch) : 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < C::NCH; ++c) {
+          uint32_t r[C::CH];
+          __syncwarp();  // tcgen05.ld is .sync.aligned: reconverge after the previous chunk's stores
+          tmem_ld_n<C::CH>(tbase + (uint32_t)(c * C::CH), r);
+          tmem_wait_ld();
+          if (c == C::NCH - 1) {  // release the accumulator (the peer's release is forwarded by its warp 1)
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (leader)
+                mbar_arrive(&acce_bar[acc]);
+              else if constexpr (C::TS)
+                mbar_arrive_cluster(acce_lead0 + 8u * (uint32_t)acc);
+              else
+                mbar_arrive(&pfree_bar[acc]);
+            }
           }
-          __syncwarp();
-          OutT* sb = reinterpret_cast<OutT*>(stage_buf + buf * C::EPI_BUF);
+          const int tc0 = t0 + c * C::CH;
+          if (C::TS && a.tma_store) {
+            if (lane == 0) {
+              if (C::EPI_NB == 2) bulk_wait_read<1>(); else bulk_wait_read<0>();
+            }
+            __syncwarp();
+            OutT* sb = reinterpret_cast<OutT*>(stage_buf + buf * C::EPI_BUF);
 #pragma unroll
-          for (int j = 0; j < C::CH; ++j) sb[j * 32 + lane] = convert_out<(OUT & 3)>(r[j], s, has_scale);
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0 && ch0 < a.n_out && tc0 < a.T) {
-            tma_store_2d(&tmY, sb, ch0, tc0);
-            bulk_commit();
-          }
-          if (C::EPI_NB == 2) buf ^= 1;
-        } else if constexpr (GATE) {
-          if constexpr (SAVE) {
-            uint8_t* pbuf = smem + (size_t)C::STAGES * C::STAGE + (size_t)(2 * part + (pchunk & 1)) * C::SAVE_BUF;
-            gate_run<DT, C::CH, true>(a, EpiCh{s, bch}, r, ch, tc0, lane, pbuf, part);
-            ++pchunk;
-          } else {
-            gate_run<DT, C::CH>(a, EpiCh{s, bch}, r, ch, tc0, lane);
-          }
-        } else if (ch_ok) {
-          if constexpr (EPI) {
-            epi_run<DT, C::CH>(a, EpiCh{s, bch}, r, (size_t)tc0 * a.n_out + ch, a.T - tc0);
-          } else {
-            OutT* yp = reinterpret_cast<OutT*>(a.Y) + (size_t)tc0 * a.n_out + ch;
-            const int nvalid = a.T - tc0;
-            if (nvalid >= C::CH) {
-#pragma unroll
-              for (int j = 0; j < C::CH; ++j) yp[(size_t)j * a.n_out] = convert_out<(OUT & 3)>(r[j], s, has_scale);
+            for (int j = 0; j < C::CH; ++j) sb[j * 32 + lane] = convert_out<(OUT & 3)>(r[j], s, has_scale);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0 && ch0 < a.n_out && tc0 < a.T) {
+              tma_store_2d(&tmY, sb, ch0, tc0);
+              bulk_commit();
+            }
+            if (C::EPI_NB == 2) buf ^= 1;
+          } else if (ch_ok) {
+            if constexpr (EPI) {
+              epi_run<DT, C::CH>(a, EpiCh{s, bch}, r, (size_t)tc0 * a.n_out + ch, a.T - tc0);
             } else {
+              OutT* yp = reinterpret_cast<OutT*>(a.Y) + (size_t)tc0 * a.n_out + ch;
+              const int nvalid = a.T - tc0;
+              if (nvalid >= C::CH) {
 #pragma unroll
-              for (int j = 0; j < C::CH; ++j)
-                if (j < nvalid) yp[(size_t)j * a.n_out] = convert_out<(OUT & 3)>(r[j], s, has_scale);
+                for (int j = 0; j < C::CH; ++j) yp[(size_t)j * a.n_out] = convert_out<(OUT & 3)>(r[j], s, has_scale);
+              } else {
+#pragma unroll
+                for (int j = 0; j < C::CH; ++j)
+                  if (j < nvalid) yp[(size_t)j * a.n_out] = convert_out<(OUT & 3)>(r[j], s, has_scale);
+              }
             }
           }
         }
