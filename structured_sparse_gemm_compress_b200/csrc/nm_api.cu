@@ -402,8 +402,9 @@ nm::Plan plan_with(const nm_handle* h, int64_t T, int sms, const Capacity& capac
     double best_cost = 1e300;
     for (int bn : cands) {
       if (forced_bn && bn != forced_bn) continue;
-      // Gated output stages read 224-token tiles in runs of 8 columns: 58.8 us against
-      // 55.9 at 192 tokens (6304 x 1024 -> 2 x 4096 bf16 2:4).
+      // The gated output stage works in steps of 16 tokens, which 192 and 128 split over
+      // four warps evenly; 224 (in runs of 8) took 58.8 us against 55.9 at 192
+      // (6304 x 1024 -> 2 x 4096 bf16 2:4).
       if (h->gated && bn == 224) continue;
       int clusters = capacity.pair[pair_slot(bn)];
       if (clusters <= 0) continue;

@@ -373,7 +373,7 @@ __device__ __forceinline__ void epi_run(const SpmmArgs& a, const EpiCh& e, const
   }
 }
 
-// ---- gated output stage (OUT has kOutGate)
+// ---- gated output stage of the one-SM kernel (OUT has kOutGate)
 //
 // p = acc * scale + bias per packed row as above, y = act(gate) * up.  A warp
 // holds 32 packed rows: lanes 0-15 the gate rows of 16 channels, lanes 16-31
@@ -496,7 +496,16 @@ __device__ __forceinline__ void gate_run(const SpmmArgs& a, const EpiCh& e, cons
 // both: no exchange between lanes.  16-bit values go to shared memory through
 // transposing 8 x 8 matrix stores, token by token, and leave in whole lines of 64
 // channels that the four warps (lane quarters) of a part fill together; one named
-// barrier per 16 tokens, two buffers.  6304 x 1024 -> 2 x 4096 bf16: see nm_gated.cu.
+// barrier per 16 tokens, two buffers.  A warp's next step is fetched from TMEM while
+// this one is computed.  bf16 2:4, us in graphs of the same call, with and without p,
+// against the lane exchange above in this kernel:
+//   6304 x 1024 -> 2 x 4096    65.4 / 51.2   (70.3 / 53.9)
+//   12608 x 768 -> 2 x 2048    56.7 / 43.8   (62.9 / 46.1)
+//   6304 x 512 -> 2 x 2048     25.3 / 22.3   (32.0 / 22.5)
+// What bounds it: L2.  At the first size 0.92 / 0.75 GB cross it (operands of every
+// tile, and the output), 14 to 15 TB/s with and without p; MMAs are active 39 / 48 %
+// of the time, instruction issue 40 / 42 %, and a fifth stage in place of a second
+// staging buffer gains nothing (52.9 without p).
 constexpr int kGateTok = 16;            // tokens of one step
 constexpr int kGateY = kGateTok * 128;  // staged Y bytes (64 channels of 16 bits; INT8 uses half)
 constexpr int kGateP = kGateTok * 256;  // staged p bytes: [token][gate, up][64 channels]
@@ -563,11 +572,12 @@ __device__ __forceinline__ void gate_piece(T* dst, const uint8_t* src, int n, bo
   }
 }
 
-// One warp's step: 16 tokens from t0 of its lane quarter's 16 channels (tile ct).
+// One warp's step: 16 tokens from t0 of its lane quarter's 16 channels (tile ct);
+// tokens at or beyond T are not stored.
 template <int DT, bool SAVE>
 __device__ __forceinline__ void gate_step(const SpmmArgs& a, const GateCh& e, const uint32_t (&rg)[8],
-                                          const uint32_t (&ru)[8], int ct, int lq, int t0, int lane, uint8_t* ybuf,
-                                          int part) {
+                                          const uint32_t (&ru)[8], int ct, int lq, int t0, int T, int lane,
+                                          uint8_t* ybuf, int part) {
   float g[8], u[8];
   gate_values<DT>(a, rg, e.sg, e.bg, g);
   gate_values<DT>(a, ru, e.su, e.bu, u);
@@ -587,7 +597,7 @@ __device__ __forceinline__ void gate_step(const SpmmArgs& a, const GateCh& e, co
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int c = ch + ((j & 2) ? 8 : 0), t = tq + (j & 1) + ((j & 4) ? 8 : 0);
-        if (c < a.n_ff && t < a.T) {
+        if (c < a.n_ff && t < T) {
           const size_t at = (size_t)t * (2 * (size_t)a.n_ff) + c;
           gate_save<DT>(a.P, at, g[j]);
           gate_save<DT>(a.P, at + a.n_ff, u[j]);
@@ -612,19 +622,19 @@ __device__ __forceinline__ void gate_step(const SpmmArgs& a, const GateCh& e, co
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int c = ch + ((j & 2) ? 8 : 0), t = tq + (j & 1) + ((j & 4) ? 8 : 0);
-      if (c < a.n_ff && t < a.T) reinterpret_cast<float*>(a.Y)[(size_t)t * a.n_ff + c] = g[j];
+      if (c < a.n_ff && t < T) reinterpret_cast<float*>(a.Y)[(size_t)t * a.n_ff + c] = g[j];
     }
   }
   named_bar_sync(1 + part, 128);  // all four lane quarters' values of these tokens are staged
   const int tid = lq * 32 + lane, c0 = ct * (kRows / 2);
   if (a.out_ty == OUT_F16 || a.out_ty == OUT_BF16) {
     const int y = tid >> 3, c = c0 + (tid & 7) * 8, t = t0 + y;
-    if (t < a.T && c < a.n_ff)
+    if (t < T && c < a.n_ff)
       gate_piece(reinterpret_cast<uint16_t*>(a.Y) + (size_t)t * a.n_ff + c,
                  ybuf + y * 128 + (((tid & 7) ^ (y & 7)) << 4), a.n_ff - c, a.n_ff % 8 == 0);
   } else if (a.out_ty == OUT_I8) {
     const int y = tid >> 2, c = c0 + (tid & 3) * 16, t = t0 + y;
-    if (tid < 64 && t < a.T && c < a.n_ff)
+    if (tid < 64 && t < T && c < a.n_ff)
       gate_piece(reinterpret_cast<uint8_t*>(a.Y) + (size_t)t * a.n_ff + c, ybuf + y * 64 + (tid & 3) * 16, a.n_ff - c,
                  a.n_ff % 16 == 0);
   }
@@ -632,7 +642,7 @@ __device__ __forceinline__ void gate_step(const SpmmArgs& a, const GateCh& e, co
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int n = tid + 128 * i, y = n >> 4, z = (n >> 3) & 1, c = c0 + (n & 7) * 8, t = t0 + y;
-      if (t < a.T && c < a.n_ff)
+      if (t < T && c < a.n_ff)
         *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.P) + (size_t)t * (2 * (size_t)a.n_ff) +
                                   (size_t)z * a.n_ff + c) =
             *reinterpret_cast<const uint4*>(pbuf + y * 256 + z * 128 + (((n & 7) ^ (y & 7)) << 4));
@@ -1477,7 +1487,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(cta_threads(OUT), 1)
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_sh;
-  __shared__ volatile int part_ok_sh[GATE ? C::EPI_WARPS / 4 : 1][2];
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -1689,23 +1698,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(cta_threads(OUT), 1)
     const int part = ew >> 2;
     uint8_t* stage_buf = smem + (size_t)C::STAGES * C::STAGE + (size_t)ew * C::EPI_NB * C::EPI_BUF;
     int buf = 0, acc = 0, iter = 0;
-    [[maybe_unused]] int step = 0;  // gated: steps staged so far
+    [[maybe_unused]] int step = 0;      // gated: steps staged so far
+    [[maybe_unused]] bool live = true;  // gated: no wait of this warp has run out
     uint32_t acc_phase = 0;
     for (int u = u_first; u < a.units; u += u_step, ++iter) {
       const int pt = u % n_pct, tt = u / n_pct;
       const int ct = 2 * pt + (int)rank;
+      [[maybe_unused]] GateCh e;
       if constexpr (GATE) {
-        // The four warps of a part meet at named barriers below: one of them waits
-        // and all take the same branch (the flag alternates between two slots).
-        if ((ew & 3) == 0) {
-          const bool got = mbar_wait_warp(&accf_bar[acc], acc_phase, &abort_sh, tmo);
-          if (lane == 0) {
-            if (!got) give_up(4);
-            part_ok_sh[part][iter & 1] = got ? 1 : 0;
-          }
+        e.fetch(a, ct * (kRows / 2) + lq * 16 + (lane >> 2));
+        // The four warps of a part meet at named barriers below, so none may leave: a
+        // warp whose wait ran out goes on without output (the later waits return at
+        // once, the kernel's error word is set).
+        if (!mbar_wait_warp(&accf_bar[acc], acc_phase, &abort_sh, tmo)) {
+          if (lane == 0 && live) give_up(4);
+          live = false;
         }
-        named_bar_sync(1 + part, 128);
-        if (!part_ok_sh[part][iter & 1]) break;
       } else {
         // No named barrier in this loop: each warp waits for the accumulator itself.
         if (!mbar_wait_warp(&accf_bar[acc], acc_phase, &abort_sh, tmo)) {
@@ -1719,22 +1727,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(cta_threads(OUT), 1)
       const int t0 = tt * BN + col0;
       const uint32_t tbase = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * BN + col0);
       if constexpr (GATE) {
-        GateCh e;
-        e.fetch(a, ct * (kRows / 2) + lq * 16 + (lane >> 2));
-#pragma unroll 1
-        for (int c = 0; c < C::WCOLS; c += kGateTok, ++step) {
-          uint32_t rg[8], ru[8];
-          __syncwarp();
-          tmem_ld16l_x16(tbase + (uint32_t)c, rg);
-          tmem_ld16l_x16(tbase + (16u << 16) + (uint32_t)c, ru);
+        uint32_t rg[2][8], ru[2][8];  // the next step's accumulators are fetched a step ahead
+        __syncwarp();
+        tmem_ld16l_x16(tbase, rg[0]);
+        tmem_ld16l_x16(tbase + (16u << 16), ru[0]);
+#pragma unroll
+        for (int i = 0; i < C::WCOLS / kGateTok; ++i, ++step) {
           tmem_wait_ld();
-          if (c + kGateTok == C::WCOLS) {  // release the accumulator (the peer's release is forwarded by its warp 1)
+          if (i + 1 < C::WCOLS / kGateTok) {
+            __syncwarp();
+            tmem_ld16l_x16(tbase + (uint32_t)((i + 1) * kGateTok), rg[(i + 1) & 1]);
+            tmem_ld16l_x16(tbase + (16u << 16) + (uint32_t)((i + 1) * kGateTok), ru[(i + 1) & 1]);
+          } else {  // release the accumulator (the peer's release is forwarded by its warp 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(leader ? &acce_bar[acc] : &pfree_bar[acc]);
           }
           uint8_t* ybuf = smem + (size_t)C::STAGES * C::STAGE + (size_t)(2 * part + (step & 1)) * C::GATE_BUF;
-          gate_step<DT, SAVE>(a, e, rg, ru, ct, lq, t0 + c, lane, ybuf, part);
+          gate_step<DT, SAVE>(a, e, rg[i & 1], ru[i & 1], ct, lq, t0 + i * kGateTok, live ? a.T : 0, lane, ybuf, part);
         }
       } else {
         const int ch0 = ct * kRows + lq * 32;
