@@ -176,6 +176,21 @@ def test_int8_output_codes():
     np.testing.assert_array_equal(Y.cpu().numpy(), np.clip(np.rint(v), -128, 127).astype(np.int8))
 
 
+@pytest.mark.parametrize("act", ACTS)
+def test_activation_of_every_fp16_value(act):
+    # p is the fp16 value itself and the up half is 1, so y is act(p) alone
+    v = torch.arange(-32768, 32768, dtype=torch.int32).to(torch.int16).view(torch.float16)
+    v = v[torch.isfinite(v)]
+    X = torch.zeros((v.numel(), 64), dtype=torch.float16)
+    X[:, 0], X[:, 4] = v, 1.0
+    W = torch.zeros((2, 64), dtype=torch.float16)
+    W[0, 0] = W[1, 4] = 1.0
+    h = nm.nm_compress_gated(W.cuda(), 4, 4)
+    y = f64(nm.nm_spmm_gated(h, X.cuda(), act=act, out="float32"))[:, 0]
+    g, tol = act_error(f64(v), 0.0, act)
+    assert (np.abs(y - g) <= tol + 1e-30).all()
+
+
 def test_extreme_gates():
     """Gates far out: the activations neither overflow nor lose their limits."""
     W = torch.zeros((2, 64), dtype=torch.float16)
