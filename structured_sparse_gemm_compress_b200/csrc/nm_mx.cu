@@ -288,9 +288,11 @@ cudaError_t launch_dequantize(const uint8_t* Q, const uint8_t* S, int64_t rows, 
 // in, over a ring of six (the time stays when scale loads, scale copies or the
 // activation's loads are left out).  12608 x 1024 -> 4096: 26.5 us for the mainloop
 // alone, 35 with bf16 output (the output stage and the mainloop share the SM's
-// shared memory and issue slots), 52.5 with bias and GELU (XU 56 %, issue 62 %).  At
-// k = 8192 it runs at 5.3 PFLOP/s.  Narrower tiles (128, 64 channels: 54 and 69 us on
-// that case) serve fewer tokens: 197 x 768 -> 2 x 2048 takes 5.4, 5.1 and 5.0 us.
+// shared memory and issue slots), 46 with bias and GELU (issue 57 %, XU 31 %, MMA 24 %:
+// the warps of a tile run through wait, arithmetic and stores together; halves of
+// them on alternate tiles took 47).  At k = 8192 it runs at 5.3 PFLOP/s.  Narrower
+// tiles (128, 64 channels: 50 and 73 us on that case) serve fewer tokens: 197 x 768 ->
+// 2 x 2048 takes 5.1 us with 192, 4.6 and 4.8 with them.
 constexpr int kMxKb = 256;
 constexpr int kMxSmemBudget = 227 * 1024 - 1024 - 512;  // 1 KB of alignment slack, barriers
 
@@ -303,7 +305,8 @@ struct MxCfg {
   static constexpr int STAGE = A_BYTES + B_BYTES + 1024 + ATOMS * 1024;
   // Accumulator columns per epilogue warp: 32, or 64 for gated tiles (32 outputs,
   // a 64-byte run of a 16-bit row).  12608 x 1024 -> 4096 with bias and GELU took
-  // 53.7 us with 32 columns a warp (24 warps of 72 registers) and 57.8 with 64.
+  // 53.7 us with 32 columns a warp (24 warps of 72 registers) and 57.8 with 64, with
+  // the GELU of gelu2.
   static constexpr int WCOLS = GATED && BN > 64 ? 64 : 32;
   static constexpr int EPW = BN / WCOLS;                       // epilogue warps per lane quarter
   static constexpr int EPI_WARPS = 4 * EPW;
@@ -343,6 +346,25 @@ __host__ __device__ constexpr uint32_t mx_idesc(uint32_t sf_id) {
   return (sf_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | (1u << 23) | ((256u >> 4) << 24) |
          (sf_id << 29);
 }
+
+// A pair's tiles, u_step apart, without a division at each (an epilogue warp of 32
+// columns runs some 500 instructions a tile).
+struct MxWalk {
+  int u, nt, mt;
+  int n_nt, du, dn, dm;
+  __device__ __forceinline__ MxWalk(int first, int step, int n)
+      : u(first), nt(first % n), mt(first / n), n_nt(n), du(step), dn(step % n), dm(step / n) {}
+  __device__ __forceinline__ int next_nt() const { return nt + dn >= n_nt ? nt + dn - n_nt : nt + dn; }
+  __device__ __forceinline__ void next() {
+    u += du;
+    nt += dn;
+    mt += dm;
+    if (nt >= n_nt) {
+      nt -= n_nt;
+      ++mt;
+    }
+  }
+};
 
 // Scale and bias of a warp's accumulator columns, one column of every 32 per lane.
 template <int WCOLS, bool GATED>
@@ -491,8 +513,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxCfg<BN, GATED>::TH
     int stage = 0;
     uint32_t phase = 0, armed = 0, armed_par = 0;
     bool ok = true;
-    for (int u = u_first; ok && u < a.units; u += u_step) {
-      const int nt = u % a.n_nt, mt = u / a.n_nt;
+    for (MxWalk w(u_first, u_step, a.n_nt); ok && w.u < a.units; w.next()) {
+      const int nt = w.nt, mt = w.mt;
       const int arow = mt * 256 + (int)rank * 128;
       // the last tile's second half may lie behind the last scale tile: any
       // tile's scales do for rows that are not stored
@@ -535,9 +557,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxCfg<BN, GATED>::TH
       int stage = 0, acc = 0, slot = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int u = u_first; ok && u < a.units; u += u_step) {
-        const int nt = u % a.n_nt;
-        const uint32_t sfb_off = (uint32_t)(((nt * BN) & 127) >> 5);  // the tile's first channel within its scale tile
+      for (MxWalk w(u_first, u_step, a.n_nt); ok && w.u < a.units; w.next()) {
+        const uint32_t sfb_off = (uint32_t)(((w.nt * BN) & 127) >> 5);  // the tile's first channel within its scale tile
         if (!mbar_wait_warp(&acce_bar[acc], acc_phase ^ 1u, &abort_sh, tmo)) {
           if (issuer) give_up(2);
           break;
@@ -597,13 +618,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxCfg<BN, GATED>::TH
     int acc = 0;
     uint32_t acc_phase = 0;
     MxVectors<C::WCOLS, GATED> vec;  // of the next tile: fetched a tile ahead
-    vec.fetch(a, (u_first % a.n_nt) * BN + part * C::WCOLS, lane);
-    for (int u = u_first; u < a.units; u += u_step) {
-      const int nt = u % a.n_nt, mt = u / a.n_nt;
-      const int row0 = mt * 256 + (int)rank * 128 + lq * 32;
-      const int col0 = nt * BN + part * C::WCOLS;
+    MxWalk w(u_first, u_step, a.n_nt);
+    vec.fetch(a, w.nt * BN + part * C::WCOLS, lane);
+    for (; w.u < a.units; w.next()) {
+      const int row0 = w.mt * 256 + (int)rank * 128 + lq * 32;
+      const int col0 = w.nt * BN + part * C::WCOLS;
       vec.publish(a, vs, vb, lane);
-      vec.fetch(a, ((u + u_step) % a.n_nt) * BN + part * C::WCOLS, lane);
+      vec.fetch(a, w.next_nt() * BN + part * C::WCOLS, lane);
       if (!mbar_wait_warp(&accf_bar[acc], acc_phase, &abort_sh, tmo)) {
         if (lane == 0) give_up(4);
         break;
