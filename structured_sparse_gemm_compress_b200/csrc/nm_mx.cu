@@ -304,9 +304,9 @@ struct MxCfg {
   static constexpr int B_BYTES = HB * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES + 1024 + ATOMS * 1024;
   // Accumulator columns per epilogue warp: 32, or 64 for gated tiles (32 outputs,
-  // a 64-byte run of a 16-bit row).  12608 x 1024 -> 4096 with bias and GELU took
-  // 53.7 us with 32 columns a warp (24 warps of 72 registers) and 57.8 with 64, with
-  // the GELU of gelu2.
+  // a 64-byte run of a 16-bit row).  12608 x 1024 -> 4096 with bias and GELU takes
+  // 45.9 us with 32 columns a warp (24 warps of 72 registers) and 47.8 with 64; gated
+  // 12608 x 768 -> 2 x 2048 33.1 with 32 and 27.3 with 64.
   static constexpr int WCOLS = GATED && BN > 64 ? 64 : 32;
   static constexpr int EPW = BN / WCOLS;                       // epilogue warps per lane quarter
   static constexpr int EPI_WARPS = 4 * EPW;
