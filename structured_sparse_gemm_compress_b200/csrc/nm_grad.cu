@@ -40,6 +40,8 @@ __device__ __forceinline__ uint16_t to_16(float v) {
   return __half_as_ushort(__float2half_rn(v));
 }
 
+// (Loads here are coherent ones: P may come from the kernel just before, beside
+// which this one may have started.)
 // Eight of this lane's columns of one row: consecutive (VEC: 16-byte accesses) or
 // 32 apart (any alignment).
 template <bool VEC>
@@ -61,7 +63,7 @@ __device__ __forceinline__ void dp_load(const uint16_t* row, int f0, int F, int 
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int f = f0 + dp_col<false>(lane, j);
-      v[j] = f < F ? to_f32<DT>(__ldg(row + f)) : 0.0f;
+      v[j] = f < F ? to_f32<DT>(__ldca(row + f)) : 0.0f;
     }
   }
 }
@@ -167,7 +169,7 @@ __device__ __forceinline__ void dbias_columns(const float* __restrict__ part, in
     for (int b = group; b < row_blocks; b += 64) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (b + 8 * i < row_blocks) run[i] += __ldg(part + (size_t)(b + 8 * i) * n + c);
+        if (b + 8 * i < row_blocks) run[i] += __ldcg(part + (size_t)(b + 8 * i) * n + c);
     }
   }
   float s = run[0];

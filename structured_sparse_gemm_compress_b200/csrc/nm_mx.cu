@@ -19,13 +19,15 @@ namespace {
 enum : int { SRC_F16 = NM_FP16, SRC_BF16 = NM_BF16, SRC_F32 = NM_FP32 };
 __host__ __device__ constexpr int src_bytes(int dt) { return dt == SRC_F32 ? 4 : 2; }
 
-// 16 consecutive values as they lie in memory, and as fp32.
+// 16 consecutive values as they lie in memory, and as fp32.  (Plain loads, here and
+// below, not the non-coherent ones: the kernel may have started while the one that
+// writes its input was running.)
 template <int DT>
 struct Raw16 {
   uint4 q[src_bytes(DT)];
   __device__ __forceinline__ void load(const void* p) {
 #pragma unroll
-    for (int i = 0; i < src_bytes(DT); ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    for (int i = 0; i < src_bytes(DT); ++i) q[i] = __ldca(reinterpret_cast<const uint4*>(p) + i);
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -201,9 +203,9 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __res
     const int64_t dst = n_ff ? gated_source_row(r, n_ff) : r;
     if (dst < 0) continue;
     const uint8_t* qp = q0 + (int64_t)dr * (k >> 1) + c * (PER / 2);
-    const uint32_t q = PER == 4 ? (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(qp))
-                                : __ldg(reinterpret_cast<const uint32_t*>(qp));
-    const uint32_t byte = __ldg(S + mx_scale_offset(r, kk >> 5, n_kb));
+    const uint32_t q = PER == 4 ? (uint32_t)__ldca(reinterpret_cast<const unsigned short*>(qp))
+                                : __ldca(reinterpret_cast<const unsigned int*>(qp));
+    const uint32_t byte = __ldca(S + mx_scale_offset(r, kk >> 5, n_kb));
     // 2^(byte - 127): a subnormal for byte 0, NaN for byte 255
     const float scale = __uint_as_float(byte == 0 ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
     float v[PER];
