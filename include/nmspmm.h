@@ -306,8 +306,8 @@ nm_status nm_compress_gated(const void* W_dev, int64_t n_ff, int64_t k, nm_dtype
  * P_dev, if not NULL, receives p itself, [T][2 n_ff] in the handle's type
  * (FP16/BF16; an INT8 handle refuses it with NM_ERR_UNSUPPORTED): what
  * nm_gated_backward needs.  16-byte aligned, overlapping neither X nor Y.
- * X, T, alignment and streams as nm_spmm.  Never allocates or synchronises and
- * keeps nothing between calls: calls on one handle may overlap.
+ * X, T (at most 2^31 - 256), alignment and streams as nm_spmm.  Never allocates or
+ * synchronises and keeps nothing between calls: calls on one handle may overlap.
  */
 nm_status nm_spmm_gated(const nm_handle* h, const void* X_dev, int64_t T, void* Y_dev, void* P_dev,
                         const nm_epilogue* ep, void* stream);

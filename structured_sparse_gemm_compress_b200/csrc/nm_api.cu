@@ -790,7 +790,8 @@ nm_status nm_spmm_gated(const nm_handle* h, const void* X, int64_t T, void* Y, v
   if (T < 0) return fail(NM_ERR_INVALID, "T must be >= 0 (got %lld)", (long long)T);
   if (T == 0) return NM_OK;
   if (!X || !Y) return fail(NM_ERR_INVALID, "null X or Y");
-  if (T > INT32_MAX) return fail(NM_ERR_UNSUPPORTED, "T above 2^31-1");
+  if (T > INT32_MAX - 255)  // a tile's last token is counted in 32 bits
+    return fail(NM_ERR_UNSUPPORTED, "T above 2^31-256");
   const int es = nm::elem_bytes(h->dt);
   if (!aligned(X, 16) || !aligned(Y, 16) || !aligned(P, 16))
     return fail(NM_ERR_INVALID, "X, Y and P must be 16-byte aligned");

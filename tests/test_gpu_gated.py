@@ -531,6 +531,7 @@ def test_refusals_on_a_handle(monkeypatch):
     fw = lambda *a: L.nm_spmm_gated(hb.raw, *a, None, None)  # noqa: E731
     assert fw(x, -1, dx, None) == nm.NM_ERR_INVALID
     assert fw(x, 1 << 31, dx, None) == nm.NM_ERR_UNSUPPORTED
+    assert fw(x, (1 << 31) - 255, dx, None) == nm.NM_ERR_UNSUPPORTED                 # the last tile's end
     assert fw(None, 8, dx, None) == nm.NM_ERR_INVALID
     assert fw(x, 8, x, None) == nm.NM_ERR_INVALID                                    # Y over X
     assert fw(x, 8, dx, dx) == nm.NM_ERR_INVALID                                     # P over Y
