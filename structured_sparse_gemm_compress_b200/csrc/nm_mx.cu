@@ -154,29 +154,33 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const uint8_t* __restr
         reinterpret_cast<const uint4*>(sc)[threadIdx.x];
 }
 
-// Four codes (the low 16 bits of q) to their values.  Every value is an fp16 number
-// whose low byte is zero, so one byte permute with the codes as selectors looks
-// four of them up; the signs are put in place bit by bit.
-__device__ __forceinline__ void e2m1x4_values(uint32_t q, float* v) {
-  // high bytes of 0, 0.5, 1, 1.5 and of 2, 3, 4, 6
-  const uint32_t mag = __byte_perm(0x3E3C3800u, 0x46444240u, q & 0x7777u);
-  const uint32_t sign = ((q << 4) & 0x80u) | ((q << 8) & 0x8000u) | ((q << 12) & 0x800000u) | ((q << 16) & 0x80000000u);
-  const uint32_t hi = mag | sign;
-  const uint32_t h[2] = {__byte_perm(hi, 0u, 0x1404u), __byte_perm(hi, 0u, 0x3424u)};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+// Four codes (the low 16 bits of q) times their block's scale (bf16, twice), as
+// bf16: exact, since bf16 holds every product (or it is infinite there and in fp32).
+// The codes are the selectors of byte permutes: two look up the bytes of the
+// magnitude, one copies 0x80 or, for a selector with its top bit set, spreads that
+// byte's sign to 0xFF, whose second highest bit is then the sign.
+__device__ __forceinline__ uint2 e2m1x4_scaled(uint32_t q, uint32_t scale2) {
+  const uint32_t sel = q & 0x7777u;
+  const uint32_t lo = prmt(0xC0800000u, 0xC0804000u, sel);  // of 0, 0.5, 1, 1.5 and of 2, 3, 4, 6
+  const uint32_t hi = prmt(0x3F3F3F00u, 0x40404040u, sel) | ((prmt(0x80808080u, 0x80808080u, q) << 1) & 0x80808080u);
+  uint2 h;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(h.x) : "r"(prmt(lo, hi, 0x5140u)), "r"(scale2));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(h.y) : "r"(prmt(lo, hi, 0x7362u)), "r"(scale2));
+  return h;
 }
 
 // A thread writes 16 bytes at a time (4 or 8 values), neighbours side by side, so
 // that a warp instruction fills whole sectors.  Block (x, y): `block_rows` rows from
 // row x * block_rows, units [y * cols, (y + 1) * cols) of each (a unit is 16 bytes
-// of output).  n_ff > 0: packed rows back to their place in W.  Bound by its
-// instructions (about 50 a unit): 7.1 us for 12608 x 768 bf16 (3.4 TB/s), 13.0 for
-// 12608 x 1024 fp32 (4.5); holding four units' loads in flight by hand changed nothing.
+// of output).  n_ff > 0: packed rows back to their place in W.  12608 x 768 bf16 takes
+// 6.3 us (3.9 TB/s; 7.2 with the values looked up as fp16 and scaled in fp32), 12608 x
+// 1024 fp32 12.4 (4.7 TB/s): launch and latency beside the bytes, four units a thread;
+// holding four units' loads in flight by hand changed nothing.
 template <int DT>
 __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __restrict__ Q,
                                                             const uint8_t* __restrict__ S, int64_t rows, int64_t k,
@@ -207,19 +211,21 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __res
                                 : __ldca(reinterpret_cast<const unsigned int*>(qp));
     const uint32_t byte = __ldca(S + mx_scale_offset(r, kk >> 5, n_kb));
     // 2^(byte - 127): a subnormal for byte 0, NaN for byte 255
-    const float scale = __uint_as_float(byte == 0 ? 0x00400000u : byte == 255u ? 0x7FC00000u : byte << 23);
-    float v[PER];
-    e2m1x4_values(q, v);
-    if constexpr (PER == 8) e2m1x4_values(q >> 16, v + 4);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = __fmul_rn(v[i], scale);
+    const uint32_t scale = byte == 0 ? 0x0040u : byte == 255u ? 0x7FC0u : byte << 7;
+    const uint32_t scale2 = scale * 0x10001u;
+    const uint2 h0 = e2m1x4_scaled(q, scale2);
     uint4 o;
     if constexpr (DT == SRC_F32) {
-      o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+      o = make_uint4(h0.x << 16, h0.x & 0xFFFF0000u, h0.y << 16, h0.y & 0xFFFF0000u);
     } else {
-      constexpr int OT = DT == SRC_F16 ? OUT_F16 : OUT_BF16;
-      o = make_uint4(pack_pair<OT>(v[0], v[1]), pack_pair<OT>(v[2], v[3]), pack_pair<OT>(v[4], v[5]),
-                     pack_pair<OT>(v[6], v[7]));
+      const uint2 h1 = e2m1x4_scaled(q >> 16, scale2);
+      o = make_uint4(h0.x, h0.y, h1.x, h1.y);
+      if constexpr (DT == SRC_F16) {
+        uint32_t* w = &o.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = pack_pair<OUT_F16>(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+      }
     }
     *reinterpret_cast<uint4*>(X + (dst * k + kk) * src_bytes(DT)) = o;
   }
