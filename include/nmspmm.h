@@ -444,8 +444,9 @@ nm_status nm_export_sizes(const nm_handle* h, size_t* values_bytes, size_t* idx_
  * INT8 fp32-output kernels) would use for T tokens on the current device,
  * without launching anything (section 4.1, mechanism 3, adaptive
  * parallelism).  For a handle from nm_compress_tile it is nm_spmm_gather's
- * plan.  Environment overrides (NMSPMM_FORCE_*) apply as they would to the
- * call.  T > 0, else NM_ERR_INVALID.
+ * plan, for one from nm_compress_gated nm_spmm_gated's without P.  Environment
+ * overrides (NMSPMM_FORCE_*) apply as they would to the call.  T > 0, else
+ * NM_ERR_INVALID.
  */
 typedef struct nm_plan_info {
   int pair;     /* 1: two-SM kernel (M = 256 per MMA, grid counts CTA pairs) */

@@ -352,8 +352,9 @@ void choose_cluster_split(const nm_handle* h, int64_t T, int sms, int forced_bn,
 
 // Adaptive parallelism: pick the kernel (CTA pair or single SM), the token tile
 // and the split-K factor for this shape (rules and their measurements below),
-// given the resident-cluster capacities.
-nm::Plan plan_with(const nm_handle* h, int64_t T, int sms, const Capacity& capacity) {
+// given the resident-cluster capacities.  save: a gated call whose p goes out in
+// whole lines.
+nm::Plan plan_with(const nm_handle* h, int64_t T, int sms, const Capacity& capacity, bool save = false) {
   nm::Plan p;
   scan_env();
   const int forced_bn = env_int("NMSPMM_FORCE_BN", 0);
@@ -397,7 +398,19 @@ nm::Plan plan_with(const nm_handle* h, int64_t T, int sms, const Capacity& capac
   const int64_t kbytes = h->k * nm::elem_bytes(h->dt);
   const bool pair_default = kbytes >= 2048 ||
                             (kbytes >= 192 && h->n_ct % 2 == 0 && (int64_t)(h->n_ct / 2) * ((T + 127) / 128) >= sms);
-  if ((forced_pair == 1 || (forced_pair == -1 && pair_default)) && forced_split <= 1 && forced_xs != 1) {
+  // Gated 16-bit products: the pair's output stage writes whole lines of y and p where
+  // the one-SM kernel's writes 16 channels at a time, so it also pays for fewer tiles.
+  // Measured in graphs (bf16 2:4 and 4:8, k = 192 .. 4096, n_ff = 448 .. 4096): with p
+  // saved, from half as many 128-token tiles as pairs on it takes 0.79-0.96 of the
+  // streaming kernel's time (1003 x 768 -> 2 x 2048: 9.0 us against 11.5), below that
+  // 0.88 to 1.25; without p, from as many tiles as pairs on, 0.82-1.03 at k >= 768 and
+  // 0.97-1.15 below; from half as many, 0.85-0.93 at k = 4096 and 0.98-1.09 up to 1024.
+  const int pair_cap = h->gated && h->dt != nm::DT_I8 ? capacity.pair[pair_slot(128)] : 0;
+  const int64_t tiles128 = (int64_t)((h->n_ct + 1) / 2) * ((T + 127) / 128);
+  const bool gated_pair = pair_cap > 0 && (save ? 2 * tiles128 >= pair_cap
+                                                : (kbytes >= 1536 && tiles128 >= pair_cap) ||
+                                                      (kbytes >= 4096 && 2 * tiles128 >= pair_cap));
+  if ((forced_pair == 1 || (forced_pair == -1 && (pair_default || gated_pair))) && forced_split <= 1 && forced_xs != 1) {
     const int cands[3] = {224, 192, 128};
     double best_cost = 1e300;
     for (int bn : cands) {
@@ -410,7 +423,7 @@ nm::Plan plan_with(const nm_handle* h, int64_t T, int sms, const Capacity& capac
       if (clusters <= 0) continue;
       if (forced_grid > 0) clusters = std::min(clusters, std::max(1, forced_grid / 2));
       const int64_t units = (int64_t)((h->n_ct + 1) / 2) * ((T + bn - 1) / bn);
-      if (forced_pair != 1 && units < clusters) continue;
+      if (forced_pair != 1 && !gated_pair && units < clusters) continue;
       const int64_t rounds = (units + clusters - 1) / clusters;
       const double cost = (double)rounds * (bn + 48);
       if (cost < best_cost) {
@@ -492,8 +505,8 @@ nm::Plan plan_with(const nm_handle* h, int64_t T, int sms, const Capacity& capac
 }
 
 // The plan for a call on this handle's device.
-nm::Plan make_plan(const nm_handle* h, int64_t T, int sms, bool scaled) {
-  return plan_with(h, T, sms, device_capacity(h, scaled));
+nm::Plan make_plan(const nm_handle* h, int64_t T, int sms, bool scaled, bool save = false) {
+  return plan_with(h, T, sms, device_capacity(h, scaled), save);
 }
 
 int out_elem_bytes(const nm_handle* h, const EpiReq* ep) {
@@ -803,7 +816,7 @@ nm_status nm_spmm_gated(const nm_handle* h, const void* X, int64_t T, void* Y, v
                                                    nm::overlaps(Y, ybytes, P, pbytes))))
     return fail(NM_ERR_INVALID, "X, Y and P overlap");
 
-  const nm::Plan p = make_plan(h, T, num_sms(h->device), false);
+  const nm::Plan p = make_plan(h, T, num_sms(h->device), false, P && h->n_out % 16 == 0);
   if (p.splits > 1 && !p.cluster)
     return fail(NM_ERR_UNSUPPORTED, "a gated product splits k on chip only (a global-memory split was forced)");
   CUtensorMap tmX;

@@ -165,6 +165,17 @@ def test_planner_splits_a_long_k_on_chip():
     assert nm.nm_plan_query(h, 16)["cluster"] == 1
 
 
+def test_planner_takes_the_pair_where_its_output_stage_pays():
+    # half as many 256-channel x 128-token tiles as pairs: with p saved only (the
+    # plan of the other calls is the one nm_plan_query reports)
+    h, _ = check_forward("bf16", 300, 768, 2048, out="default", save=True)
+    assert nm.nm_plan_query(h, 300)["pair"] == 0
+    h, _ = check_forward("fp16", 790, 768, 2048, out="default")
+    assert nm.nm_plan_query(h, 790)["pair"] == 1
+    h, _ = check_forward("bf16", 301, 2048, 2056, N=4, M=8, out="default")   # an odd number of 128-row tiles
+    assert nm.nm_plan_query(h, 301)["pair"] == 1
+
+
 def test_int8_output_codes():
     """Without an activation the arithmetic is fixed: the codes are exact."""
     X, W, s, b = problem("int8", 75, 256, 41, 2, 4)
