@@ -344,6 +344,7 @@ struct MxArgs {
   int n_nt, units;
   int out_ty, act;
   int vec;                   // rows of Y start on 16 bytes
+  int a_rows;                // token rows of a copy of X
   unsigned long long timeout_ns;
 };
 
@@ -518,6 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxCfg<BN, GATED>::TH
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)
     const bool issuer = elect_one();
+    const uint32_t stage_tx = 2u * (uint32_t)(C::STAGE - C::A_BYTES + a.a_rows * 128);
     int stage = 0;
     uint32_t phase = 0, armed = 0, armed_par = 0;
     bool ok = true;
@@ -538,7 +540,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxCfg<BN, GATED>::TH
         if (issuer) {
           uint8_t* st = smem + (size_t)stage * C::STAGE;
           const uint32_t fb = full_lead0 + 8u * (uint32_t)stage;
-          if (leader) mbar_arrive_expect_tx(&full_bar[stage], (uint32_t)(2 * C::STAGE));
+          if (leader) mbar_arrive_expect_tx(&full_bar[stage], stage_tx);
           tma_load_2d_pair(st, &tmA, fb, kb * 128, arow);
           tma_load_2d_pair(st + C::A_BYTES, &tmB, fb, kb * 128, brow);
           tma_load_2d_pair(st + C::A_BYTES + C::B_BYTES, &tmSA, fb, 0, (stile * a.n_kb + kb) * 8);
@@ -800,7 +802,11 @@ nm_status mx_product(const nm_handle* h, const void* Q, const void* S, int64_t T
   a.units = (int)units;
 
   CUtensorMap tmA, tmSA;
-  if ((st = codes_map(&tmA, Q, T, h->k, 128)) != NM_OK) return st;
+  // Fewer than 128 tokens: the copies bring in those rows alone (whole swizzle groups
+  // of 8).  The operand's other rows hold what the stage held before; they reach
+  // only accumulator rows that are not stored.
+  a.a_rows = T < 128 ? (int)((T + 7) / 8 * 8) : 128;
+  if ((st = codes_map(&tmA, Q, T, h->k, a.a_rows)) != NM_OK) return st;
   if ((st = scales_map(&tmSA, S, (int64_t)sbytes)) != NM_OK) return st;
   a.vec = (n_y * es) % 16 == 0 ? 1 : 0;
   const int grid = (int)(units < pairs ? units : pairs);
