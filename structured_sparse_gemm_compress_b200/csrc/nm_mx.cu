@@ -291,16 +291,14 @@ cudaError_t launch_dequantize(const uint8_t* Q, const uint8_t* S, int64_t rows, 
 // two halves of a gated pair (16 gate channels beside their 16 up channels) meet
 // in one thread, and rows leave through a staged tile as whole lines.
 //
-// What bounds it.  A stage (256 k of a 192-channel tile) takes 490-510 cycles against
-// 384 of MMA: 31 KB a stage and SM at the ~70 bytes a cycle that tensor copies bring
-// in, over a ring of six (the time stays when scale loads, scale copies or the
-// activation's loads are left out).  12608 x 1024 -> 4096: 26.5 us for the mainloop
-// alone, 35 with bf16 output (the output stage and the mainloop share the SM's
-// shared memory and issue slots), 46 with bias and GELU (issue 57 %, XU 31 %, MMA 24 %:
-// the warps of a tile run through wait, arithmetic and stores together; halves of
-// them on alternate tiles took 47).  At k = 8192 it runs at 5.3 PFLOP/s.  Narrower
-// tiles (128, 64 channels: 50 and 73 us on that case) serve fewer tokens: 197 x 768 ->
-// 2 x 2048 takes 5.1 us with 192, 4.6 and 4.8 with them.
+// What bounds it.  A stage (256 k of a 192-channel tile) takes 0.22 us, 430 cycles
+// against 384 of MMA; a 64-channel tile's takes 0.21, the issuing lane's own
+// instructions.  12608 x 1024 -> 4096: 35 us with bf16 output (the output stage and the
+// mainloop share the SM's shared memory and issue slots), 45 with bias and GELU (issue
+// 58 %, XU 28 %, MMA 25 %: the warps of a tile run through wait, arithmetic and stores
+// together; halves of them on alternate tiles took 47 against 46 then).  At k = 8192 it
+// runs at 5.6 PFLOP/s.  Narrower tiles (128, 64 channels: 47 and 58 us on that case)
+// serve fewer tokens: 197 x 768 -> 2 x 2048 takes 5.0 us with 192, 4.5 and 4.6 with them.
 constexpr int kMxKb = 256;
 constexpr int kMxSmemBudget = 227 * 1024 - 1024 - 512;  // 1 KB of alignment slack, barriers
 
@@ -518,105 +516,124 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MxCfg<BN, GATED>::TH
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)
-    const bool issuer = elect_one();
-    const uint32_t stage_tx = 2u * (uint32_t)(C::STAGE - C::A_BYTES + a.a_rows * 128);
-    int stage = 0;
-    uint32_t phase = 0, armed = 0, armed_par = 0;
-    bool ok = true;
-    for (MxWalk w(u_first, u_step, a.n_nt); ok && w.u < a.units; w.next()) {
-      const int nt = w.nt, mt = w.mt;
-      const int arow = mt * 256 + (int)rank * 128;
-      // the last tile's second half may lie behind the last scale tile: any
-      // tile's scales do for rows that are not stored
-      const int stile = min(2 * mt + (int)rank, a.n_tb - 1);
-      const int brow = nt * BN + (int)rank * C::HB;
-      const int btile = (nt * BN) >> 7;
-      for (int kb = 0; kb < a.n_kb; ++kb) {
-        if (!mbar_wait_warp(&empty_bar[stage], phase ^ 1u, &abort_sh, tmo)) {
-          if (issuer) give_up(1);
-          ok = false;
-          break;
-        }
-        if (issuer) {
-          uint8_t* st = smem + (size_t)stage * C::STAGE;
-          const uint32_t fb = full_lead0 + 8u * (uint32_t)stage;
-          if (leader) mbar_arrive_expect_tx(&full_bar[stage], stage_tx);
-          tma_load_2d_pair(st, &tmA, fb, kb * 128, arow);
-          tma_load_2d_pair(st + C::A_BYTES, &tmB, fb, kb * 128, brow);
-          tma_load_2d_pair(st + C::A_BYTES + C::B_BYTES, &tmSA, fb, 0, (stile * a.n_kb + kb) * 8);
-#pragma unroll
-          for (int i = 0; i < C::ATOMS; ++i)
-            tma_load_2d_pair(st + C::A_BYTES + C::B_BYTES + 1024 + i * 1024, &tmSB, fb, 0,
-                             (min(btile + i, a.n_rb - 1) * a.n_kb + kb) * 8);
-        }
-        armed |= 1u << stage;
-        armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
-        if (++stage == C::STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    if (leader)  // drain: both CTAs' copies have landed (the peer is held by the cluster barrier below)
-      for (int i = 0; i < C::STAGES; ++i)
-        if ((armed >> i) & 1u) mbar_wait_warp(&full_bar[i], (armed_par >> i) & 1u, &abort_sh, tmo);
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (leader only)
-    if (leader) {
-      const bool issuer = elect_one();
-      int stage = 0, acc = 0, slot = 0;
-      uint32_t phase = 0, acc_phase = 0;
+    // One lane runs this loop, and one the next: with whole warps around the issuing
+    // lane, their instructions made a stage take 0.25 us whatever the tile's width
+    // (0.21 so; three stages in the ring were as good as eight).
+    uint32_t issued = 0;
+    if (elect_one()) {
+      const uint32_t stage_tx = 2u * (uint32_t)(C::STAGE - C::A_BYTES + a.a_rows * 128);
+      int stage = 0;
+      uint32_t phase = 0;
       bool ok = true;
+      uint8_t* st = smem;
+      uint32_t fb = full_lead0;
       for (MxWalk w(u_first, u_step, a.n_nt); ok && w.u < a.units; w.next()) {
-        const uint32_t sfb_off = (uint32_t)(((w.nt * BN) & 127) >> 5);  // the tile's first channel within its scale tile
-        if (!mbar_wait_warp(&acce_bar[acc], acc_phase ^ 1u, &abort_sh, tmo)) {
-          if (issuer) give_up(2);
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem + (uint32_t)(acc * BN);
+        const int arow = w.mt * 256 + (int)rank * 128;
+        const int brow = w.nt * BN + (int)rank * C::HB;
+        const int btile = (w.nt * BN) >> 7;
+        // the last tile's second half may lie behind the last scale tile: any
+        // tile's scales do for rows that are not stored
+        const int srow = min(2 * w.mt + (int)rank, a.n_tb - 1) * a.n_kb * 8;
+        int brow8[C::ATOMS];
+#pragma unroll
+        for (int i = 0; i < C::ATOMS; ++i) brow8[i] = min(btile + i, a.n_rb - 1) * a.n_kb * 8;
         for (int kb = 0; kb < a.n_kb; ++kb) {
-          if (!mbar_wait_warp(&full_bar[stage], phase, &abort_sh, tmo)) {
-            if (issuer) give_up(3);
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &abort_sh, tmo)) {
+            give_up(1);
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + (size_t)stage * C::STAGE);
-          const uint32_t b_addr = a_addr + C::A_BYTES, sa_addr = b_addr + C::B_BYTES, sb_addr = sa_addr + 1024;
-          const uint32_t sfa = tmem + (uint32_t)(2 * BN + slot * C::SF_COLS), sfb = sfa + 8;
-          const uint64_t ad0 = sdesc_sw128(a_addr), bd0 = sdesc_sw128(b_addr);
-          const int mmas = min(4, (a.k - kb * kMxKb + 63) >> 6);  // k beyond the matrix is skipped in steps of 64
-          if (issuer) {
+          if (leader) mbar_arrive_expect_tx(&full_bar[stage], stage_tx);
+          tma_load_2d_pair(st, &tmA, fb, kb * 128, arow);
+          tma_load_2d_pair(st + C::A_BYTES, &tmB, fb, kb * 128, brow);
+          tma_load_2d_pair(st + C::A_BYTES + C::B_BYTES, &tmSA, fb, 0, srow + kb * 8);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              tc_cp_32x128b_x4_pair(sfa + 4 * h, sdesc_rows16(sa_addr + 512 * h));
-#pragma unroll
-              for (int i = 0; i < C::ATOMS; ++i)
-                tc_cp_32x128b_x4_pair(sfb + 4 * C::ATOMS * h + 4 * i, sdesc_rows16(sb_addr + 1024 * i + 512 * h));
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (j < mmas)
-                tc_mma_mxf4_pair(d_tmem, ad0 + 2u * j, bd0 + 2u * j, (j & 1) ? mx_idesc<BN>(2) : mx_idesc<BN>(0),
-                                 sfa + 4 * (j >> 1), sfb + 4 * C::ATOMS * (j >> 1) + sfb_off,
-                                 (kb > 0 || j > 0) ? 1u : 0u);
-            tc_commit_pair(&empty_bar[stage], (uint16_t)3);
-          }
-          slot ^= 1;
+          for (int i = 0; i < C::ATOMS; ++i)
+            tma_load_2d_pair(st + C::A_BYTES + C::B_BYTES + 1024 + i * 1024, &tmSB, fb, 0, brow8[i] + kb * 8);
+          ++issued;
+          st += C::STAGE;
+          fb += 8;
           if (++stage == C::STAGES) {
             stage = 0;
+            st = smem;
+            fb = full_lead0;
             phase ^= 1u;
           }
         }
-        if (!ok) break;
-        if (issuer) tc_commit_pair(&accf_bar[acc], (uint16_t)3);
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
       }
-      if (issuer) tc_commit_pair(&drain_bar, (uint16_t)3);
+      if (leader)  // drain: both CTAs' copies have landed (the peer is held by the cluster barrier below)
+        for (uint32_t i = issued > (uint32_t)C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
+          mbar_wait(&full_bar[i % C::STAGES], (i / C::STAGES) & 1u, &abort_sh, tmo);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (leader only)
+    if (leader) {
+      if (elect_one()) {
+        int stage = 0, acc = 0, slot = 0;
+        uint32_t phase = 0, acc_phase = 0, off = 0;  // off: the stage's offset in the descriptors' address fields
+        const uint32_t base = smem_u32(smem);
+        const uint64_t ad_base = sdesc_sw128(base), bd_base = sdesc_sw128(base + C::A_BYTES);
+        const uint64_t sa_base = sdesc_rows16(base + C::A_BYTES + C::B_BYTES);
+        bool ok = true;
+        for (MxWalk w(u_first, u_step, a.n_nt); ok && w.u < a.units; w.next()) {
+          const uint32_t sfb_off = (uint32_t)(((w.nt * BN) & 127) >> 5);  // the tile's first channel within its scale tile
+          if (!mbar_wait(&acce_bar[acc], acc_phase ^ 1u, &abort_sh, tmo)) {
+            give_up(2);
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem + (uint32_t)(acc * BN);
+          for (int kb = 0; kb < a.n_kb; ++kb) {
+            if (!mbar_wait(&full_bar[stage], phase, &abort_sh, tmo)) {
+              give_up(3);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t ad0 = ad_base + off, bd0 = bd_base + off, sa0 = sa_base + off;
+            const uint32_t sfa = tmem + (uint32_t)(2 * BN + slot * C::SF_COLS), sfb = sfa + 8;
+            const int mmas = min(4, (a.k - kb * kMxKb + 63) >> 6);  // k beyond the matrix is skipped in steps of 64
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              tc_cp_32x128b_x4_pair(sfa + 4 * h, sa0 + 32u * h);
+#pragma unroll
+              for (int i = 0; i < C::ATOMS; ++i)
+                tc_cp_32x128b_x4_pair(sfb + 4 * C::ATOMS * h + 4 * i, sa0 + 64u + 64u * i + 32u * h);
+            }
+            if (mmas == 4) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                tc_mma_mxf4_pair(d_tmem, ad0 + 2u * j, bd0 + 2u * j, (j & 1) ? mx_idesc<BN>(2) : mx_idesc<BN>(0),
+                                 sfa + 4 * (j >> 1), sfb + 4 * C::ATOMS * (j >> 1) + sfb_off,
+                                 (kb > 0 || j > 0) ? 1u : 0u);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 3; ++j)
+                if (j < mmas)
+                  tc_mma_mxf4_pair(d_tmem, ad0 + 2u * j, bd0 + 2u * j, (j & 1) ? mx_idesc<BN>(2) : mx_idesc<BN>(0),
+                                   sfa + 4 * (j >> 1), sfb + 4 * C::ATOMS * (j >> 1) + sfb_off,
+                                   (kb > 0 || j > 0) ? 1u : 0u);
+            }
+            tc_commit_pair(&empty_bar[stage], (uint16_t)3);
+            slot ^= 1;
+            off += C::STAGE >> 4;
+            if (++stage == C::STAGES) {
+              stage = 0;
+              off = 0;
+              phase ^= 1u;
+            }
+          }
+          if (!ok) break;
+          tc_commit_pair(&accf_bar[acc], (uint16_t)3);
+          if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1u;
+          }
+        }
+        tc_commit_pair(&drain_bar, (uint16_t)3);
+      }
+      __syncwarp();
     }
     mbar_wait_warp(&drain_bar, 0, &abort_sh, tmo);  // every MMA of this pair has completed
   } else {
