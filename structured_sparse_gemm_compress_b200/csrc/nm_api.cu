@@ -405,7 +405,9 @@ nm::Plan plan_with(const nm_handle* h, int64_t T, int sms, const Capacity& capac
   // streaming kernel's time (1003 x 768 -> 2 x 2048: 9.0 us against 11.5), below that
   // 0.88 to 1.25; without p, from as many tiles as pairs on, 0.82-1.03 at k >= 768 and
   // 0.97-1.15 below; from half as many, 0.85-0.93 at k = 4096 and 0.98-1.09 up to 1024.
-  const int pair_cap = h->gated && h->dt != nm::DT_I8 ? capacity.pair[pair_slot(128)] : 0;
+  // A single 128-row tile leaves half of every pair tile empty (25216 x 768 -> 2 x 64:
+  // 11.2 us against 8.0 without p, 11.8 against 9.8 with it); three already pay.
+  const int pair_cap = h->gated && h->dt != nm::DT_I8 && h->n_ct > 1 ? capacity.pair[pair_slot(128)] : 0;
   const int64_t tiles128 = (int64_t)((h->n_ct + 1) / 2) * ((T + 127) / 128);
   const bool gated_pair = pair_cap > 0 && (save ? 2 * tiles128 >= pair_cap
                                                 : (kbytes >= 1536 && tiles128 >= pair_cap) ||

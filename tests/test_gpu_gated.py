@@ -174,6 +174,8 @@ def test_planner_takes_the_pair_where_its_output_stage_pays():
     assert nm.nm_plan_query(h, 790)["pair"] == 1
     h, _ = check_forward("bf16", 301, 2048, 2056, N=4, M=8, out="default")   # an odd number of 128-row tiles
     assert nm.nm_plan_query(h, 301)["pair"] == 1
+    h, _ = check_forward("bf16", 9600, 768, 64, out="default", save=True)    # one tile: half a pair
+    assert nm.nm_plan_query(h, 9600)["pair"] == 0
 
 
 def test_int8_output_codes():
