@@ -213,6 +213,14 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 // Wait until the previous kernel of the stream has completed and its memory
 // operations are visible (returns at once when there is none).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A load of global memory that the previous kernel of the stream may have written while
+// this one was already resident: what a kernel launched by launch_pdl reads is not
+// read-only for that kernel's lifetime, which the non-coherent path (__ldg, and plain loads
+// through a const __restrict__ pointer) asks for.
+template <typename T>
+__device__ __forceinline__ T ld_coherent(const T* p) {
+  return __ldca(p);
+}
 
 // --- thread-block clusters (CTA pairs)
 

@@ -19,9 +19,8 @@ namespace {
 enum : int { SRC_F16 = NM_FP16, SRC_BF16 = NM_BF16, SRC_F32 = NM_FP32 };
 __host__ __device__ constexpr int src_bytes(int dt) { return dt == SRC_F32 ? 4 : 2; }
 
-// 16 consecutive values as they lie in memory, and as fp32.  (Plain loads, here and
-// below, not the non-coherent ones: the kernel may have started while the one that
-// writes its input was running.)
+// 16 consecutive values as they lie in memory, and as fp32.  (Coherent loads, here and
+// below: the kernel may have started while the one that writes its input was running.)
 template <int DT>
 struct Raw16 {
   uint4 q[src_bytes(DT)];
@@ -388,8 +387,8 @@ struct MxVectors {
         in = f < a.n_ff;
         src = (ch & 16) ? a.n_ff + f : f;
       }
-      s[c] = a.scale && in ? __ldg(a.scale + src) : 0.0f;
-      b[c] = a.bias && in ? __ldg(a.bias + src) : 0.0f;
+      s[c] = a.scale && in ? ld_coherent(a.scale + src) : 0.0f;
+      b[c] = a.bias && in ? ld_coherent(a.bias + src) : 0.0f;
     }
   }
   // Into shared memory, where every lane reads them all.

@@ -516,10 +516,10 @@ struct GateCh {  // a thread's two channels c and c + 8
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const bool in = c + 8 * i < a.n_ff;
-      sg[i] = a.scale && in ? __ldg(a.scale + c + 8 * i) : 1.0f;
-      su[i] = a.scale && in ? __ldg(a.scale + a.n_ff + c + 8 * i) : 1.0f;
-      bg[i] = a.bias && in ? __ldg(a.bias + c + 8 * i) : 0.0f;
-      bu[i] = a.bias && in ? __ldg(a.bias + a.n_ff + c + 8 * i) : 0.0f;
+      sg[i] = a.scale && in ? ld_coherent(a.scale + c + 8 * i) : 1.0f;
+      su[i] = a.scale && in ? ld_coherent(a.scale + a.n_ff + c + 8 * i) : 1.0f;
+      bg[i] = a.bias && in ? ld_coherent(a.bias + c + 8 * i) : 0.0f;
+      bu[i] = a.bias && in ? ld_coherent(a.bias + a.n_ff + c + 8 * i) : 0.0f;
     }
   }
 };
@@ -723,8 +723,8 @@ __device__ __forceinline__ void csplit_reduce(const SpmmArgs& a, const Unit& w, 
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const bool ok = ch + i < a.n_out;
-    sc[i] = (has_scale && ok) ? __ldg(a.scale + ch + i) : 1.0f;
-    bi[i] = (EPI && a.bias && ok) ? __ldg(a.bias + ch + i) : 0.0f;
+    sc[i] = (has_scale && ok) ? ld_coherent(a.scale + ch + i) : 1.0f;
+    bi[i] = (EPI && a.bias && ok) ? ld_coherent(a.bias + ch + i) : 0.0f;
   }
   if (ch >= a.n_out) return;
 #pragma unroll 1
@@ -789,10 +789,10 @@ __device__ __forceinline__ void csplit_reduce_gated(const SpmmArgs& a, const Uni
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const bool ok = ch + i < a.n_ff;
-    eg[i].s = (a.scale && ok) ? __ldg(a.scale + ch + i) : 1.0f;
-    eu[i].s = (a.scale && ok) ? __ldg(a.scale + a.n_ff + ch + i) : 1.0f;
-    eg[i].b = (a.bias && ok) ? __ldg(a.bias + ch + i) : 0.0f;
-    eu[i].b = (a.bias && ok) ? __ldg(a.bias + a.n_ff + ch + i) : 0.0f;
+    eg[i].s = (a.scale && ok) ? ld_coherent(a.scale + ch + i) : 1.0f;
+    eu[i].s = (a.scale && ok) ? ld_coherent(a.scale + a.n_ff + ch + i) : 1.0f;
+    eg[i].b = (a.bias && ok) ? ld_coherent(a.bias + ch + i) : 0.0f;
+    eu[i].b = (a.bias && ok) ? ld_coherent(a.bias + a.n_ff + ch + i) : 0.0f;
   }
 #pragma unroll 1
   for (int j = w.z + S * (2 * ew + (lane >> 4)); j < BN; j += 2 * S * EPI_WARPS) {
@@ -967,7 +967,7 @@ __global__ void __launch_bounds__(kernel_threads(IMG, OUT), 1)
           int4 grow = make_int4(0, 0, 0, 0);
           if constexpr (C::GA) {
             if (a.gather_tma && lane < C::KB / 4)
-              grow = __ldg(reinterpret_cast<const int4*>(a.kidx + ((size_t)w.ct * a.n_kb + kb) * C::KB) + lane);
+              grow = ld_coherent(reinterpret_cast<const int4*>(a.kidx + ((size_t)w.ct * a.n_kb + kb) * C::KB) + lane);
           }
           if (!mbar_wait_warp(&empty_bar[stage], phase ^ 1u, &abort_sh, tmo)) {
             if (issuer) give_up(1);
@@ -1151,7 +1151,7 @@ __global__ void __launch_bounds__(kernel_threads(IMG, OUT), 1)
             int rows[PASSES];
             const int32_t* kl = a.kidx + ((size_t)w.ct * a.n_kb + kb) * C::KB + rsub;
 #pragma unroll
-            for (int i = 0; i < PASSES; ++i) rows[i] = __ldg(kl + i * RSTEP);
+            for (int i = 0; i < PASSES; ++i) rows[i] = ld_coherent(kl + i * RSTEP);
             if (!mbar_wait_warp(&empty_bar[stage], phase ^ 1u, &abort_sh, tmo)) {
               if (lane == 0) give_up(1);
               ok = false;
@@ -1239,8 +1239,8 @@ __global__ void __launch_bounds__(kernel_threads(IMG, OUT), 1)
       const int wrow = GATE ? (int)gated_source_row(ch, a.n_ff) : ch;
       const bool ch_ok = GATE ? wrow >= 0 : ch < a.n_out;
       const bool has_scale = a.scale != nullptr;
-      const float s = (has_scale && ch_ok) ? __ldg(a.scale + wrow) : 1.0f;
-      const float bch = (EPI && a.bias && ch_ok) ? __ldg(a.bias + wrow) : 0.0f;
+      const float s = (has_scale && ch_ok) ? ld_coherent(a.scale + wrow) : 1.0f;
+      const float bch = (EPI && a.bias && ch_ok) ? ld_coherent(a.bias + wrow) : 0.0f;
       const int col0 = part * C::WCOLS;        // first token column of this warp within the tile
       const int t0 = w.tt * BN + col0;
       const uint32_t tbase = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * BN + col0);
@@ -1751,8 +1751,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(cta_threads(OUT), 1)
         const int ch = ch0 + lane;
         const bool ch_ok = ch < a.n_out;
         const bool has_scale = a.scale != nullptr;
-        const float s = (has_scale && ch_ok) ? __ldg(a.scale + ch) : 1.0f;
-        const float bch = (EPI && a.bias && ch_ok) ? __ldg(a.bias + ch) : 0.0f;
+        const float s = (has_scale && ch_ok) ? ld_coherent(a.scale + ch) : 1.0f;
+        const float bch = (EPI && a.bias && ch_ok) ? ld_coherent(a.bias + ch) : 0.0f;
 #pragma unroll 1
         for (int c = 0; c < C::NCH; ++c) {
           uint32_t r[C::CH];

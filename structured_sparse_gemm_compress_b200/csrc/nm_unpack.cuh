@@ -42,7 +42,8 @@ __device__ __forceinline__ void unpack16(uint4 q, T* v) {
 }
 
 // 16 consecutive dense k positions (k0 a multiple of 16) of W's row r, decoded from
-// the packed image into Wout [rows][K].  n_ff > 0: a gated weight.
+// the packed image into Wout [rows][K].  n_ff > 0: a gated weight.  (Coherent loads: the
+// image may come from the kernel just before.)
 template <int DT>
 __device__ __forceinline__ void unpack_unit(const uint8_t* __restrict__ bpack, int64_t n_ff, int64_t K, int img, int n_kb,
                                             typename Elem<DT>::T* __restrict__ Wout, int64_t r, int64_t k0) {
@@ -61,13 +62,13 @@ __device__ __forceinline__ void unpack_unit(const uint8_t* __restrict__ bpack, i
   if (img == IMG_SP24) {
     T comp[8];
     if (ES == 1) {
-      const uint64_t v = *reinterpret_cast<const uint64_t*>(chunk + swz128(rr, kk / 2));
+      const unsigned long long v = ld_coherent(reinterpret_cast<const unsigned long long*>(chunk + swz128(rr, kk / 2)));
 #pragma unroll
       for (int e = 0; e < 8; ++e) comp[e] = (T)(int8_t)(uint8_t)(v >> (8 * e));
     } else {
-      unpack16<T>(*reinterpret_cast<const uint4*>(chunk + swz128(rr, kk)), comp);
+      unpack16<T>(ld_coherent(reinterpret_cast<const uint4*>(chunk + swz128(rr, kk))), comp);
     }
-    const uint32_t meta = *reinterpret_cast<const uint16_t*>(chunk + kAtomBytes + meta_off16(DT, rr, kk));
+    const uint32_t meta = ld_coherent(reinterpret_cast<const uint16_t*>(chunk + kAtomBytes + meta_off16(DT, rr, kk)));
     // positions of a group's two slots always differ; selects keep `out` in registers
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -80,7 +81,7 @@ __device__ __forceinline__ void unpack_unit(const uint8_t* __restrict__ bpack, i
 #pragma unroll
     for (int h = 0; h < ES; ++h) {
       const uint32_t byte = kk * ES + 16u * h;
-      unpack16<T>(*reinterpret_cast<const uint4*>(chunk + (byte >> 7) * kAtomBytes + swz128(rr, byte & 127u)),
+      unpack16<T>(ld_coherent(reinterpret_cast<const uint4*>(chunk + (byte >> 7) * kAtomBytes + swz128(rr, byte & 127u))),
                   out + h * (16 / ES));
     }
   }
