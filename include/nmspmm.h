@@ -134,7 +134,10 @@ nm_status nm_recompress(nm_handle* h, const void* W_dev, void* stream);
  *                                       (round-to-nearest, one multiply);
  *             FP16/BF16               : same dtype as X, rounded to nearest
  *                                       once from the fp32 accumulator
- *                                       (times scale[n] when given).
+ *                                       (times scale[n] when given).  The
+ *                                       accumulator is the tensor core's, which
+ *                                       truncates: it is within (k / 8 + 4) 2^-23
+ *                                       sum |x| |w| of the exact sum.
  *           Must be 16-byte aligned and must not overlap X.
  * scale_dev float32 [n_out] or NULL.
  * T         >= 0; T == 0 is a no-op returning NM_OK.
@@ -296,8 +299,8 @@ nm_status nm_compress_gated(const void* W_dev, int64_t n_ff, int64_t k, nm_dtype
  * kernel:
  *   p[t][r] = acc(X . Wm^T)[t][r] * scale[r] + bias[r]      r in [0, 2 n_ff)
  *   Y[t][f] = act(p[t][f]) * p[t][n_ff + f]                 f in [0, n_ff)
- * in fp32, each step rounded to nearest as in nm_spmm_ex, Y rounded once to its
- * type.  act is any nm_act.  ep->scale and ep->bias are [2 n_ff] (or NULL);
+ * with acc the accumulator of nm_spmm, in fp32, each step rounded to nearest as in
+ * nm_spmm_ex, Y rounded once to its type.  act is any nm_act.  ep->scale and ep->bias are [2 n_ff] (or NULL);
  * output types, errors and defaults are nm_spmm_ex's, but NM_OUT_INT32 is
  * refused, and the default of an INT8 handle is fp32.  ep == NULL: NM_ACT_SILU,
  * default output.  The SiLU is within (6e-7 + 1.3e-7 max(0, -v)) |SiLU(v)| +
@@ -326,7 +329,11 @@ nm_status nm_spmm_gated(const nm_handle* h, const void* X_dev, int64_t T, void* 
  * dX and dW have the handle's type.  dp is computed in fp32; the two products
  * read it rounded to the handle's type (their tensor-core operand), sum in fp32
  * and round once; dbias sums the unrounded fp32 values, in a fixed order.
- * Results do not depend on timing.
+ * Results do not depend on timing.  The tensor core truncates its accumulator, so
+ * one holds at most 2^14 products; the runs of a longer sum are added in fp32,
+ * rounded to nearest.  With h half a unit of the handle's type (2^-11, 2^-8) and A
+ * the sum of |dp| |Wm| (dW: |dp| |X|) over the n = 2 n_ff (dW: T) terms, a result r
+ * is within (h + min(n, 2^14) 2^-26 + 2^-17 + n 2^-38) A + h |r| of the exact one.
  *
  * dX_dev, dW_dev, dbias_dev: any may be NULL (not computed), not all three.
  * X_dev [T][k] (needed for dW only, else may be NULL), P_dev [T][2 n_ff],
@@ -401,8 +408,9 @@ nm_status nm_compress_mx(const void* W_dev, int64_t n_out, int64_t k, nm_dtype d
 /*
  * nm_spmm_mx -- Y = X . Wm^T with X given quantised (codes Q_dev [T][k / 2] and
  * scales S_dev of nm_mx_quantize) and the handle's quantised weight: products
- * of 4-bit values times their blocks' scales, summed in fp32, then the fused
- * output stage of nm_spmm_ex (scale, bias, NM_ACT_GELU; fp32, fp16 or bf16).
+ * of 4-bit values times their blocks' scales, summed in fp32 (by the tensor core,
+ * within (k / 32 + 4) 2^-23 sum |x| |w|), then the fused output stage of
+ * nm_spmm_ex (scale, bias, NM_ACT_GELU; fp32, fp16 or bf16).
  * NM_OUT_DEFAULT is the type of the handle's source weight; ep == NULL is that
  * with nothing else.  Y_dev [T][n_out], 16-byte aligned, overlapping neither Q
  * nor S; T >= 0 (0 is a no-op).  Allocates nothing, never synchronises, keeps

@@ -204,7 +204,15 @@ __global__ void __launch_bounds__(128) dbias_kernel(const float* __restrict__ pa
 // the power cap, 0.33 over seconds; 6304 x 1024 -> 2 x 4096 takes 154 us (1370
 // TFLOP/s, 1.48 GHz at 990 W).  Where few pairs work, a 128-wide stage takes
 // 0.19-0.2 us, the round trip of a copy over the eight stages in flight.
+//
+// Long sums.  The tensor core truncates its fp32 accumulator: a step of 16 products
+// loses half a unit in the last place on average, so same-sign sums of n products came
+// out n / 16 x 2^-24 low (0.17 % at n = 2^18, 0.67 % at 2^20).  An accumulator therefore
+// takes kRunKb stages at most, 2^14 products (1.0e-4 low at worst-case signs, a fifth of
+// fp16's half unit); the epilogue adds the runs of a longer sum in fp32, rounded to
+// nearest, in order.
 constexpr int kGradKb = 64;
+constexpr int kRunKb = 256;
 constexpr int kGradEpiWarps = 8;
 constexpr int kGradThreads = 64 + 32 * kGradEpiWarps;
 
@@ -244,6 +252,7 @@ struct GradArgs {
   // Where few tiles have long sums, a tile is cut into parts on several pairs: they
   // leave fp32 tiles in `partial` ([slot][256][BN]) and grad_join_kernel adds them up.
   float* partial;
+  float* runs;             // sums of more than kRunKb stages: each epilogue warp's columns so far
   void *dW, *dX;
   const float* part;       // with dbias: the row blocks' column sums, row_blocks of them
   float* dbias;
@@ -411,41 +420,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int i = 0; ok && grad_unit(a, pair, pairs, i, BN, u); ++i) {
-        if (!mbar_wait_warp(&acce_bar[acc], acc_phase ^ 1u, &abort_sh, tmo)) {
-          if (issuer) give_up(2);
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem + (uint32_t)(acc * BN);
         const uint32_t idesc = u.dw ? grad_idesc<DT, BN>(true) : grad_idesc<DT, BN>(false);
         // per MMA (16 summed elements): 32 bytes along a K-major row, 16 rows of an MN-major run
         const uint64_t a_step = u.dw ? (16u * 128u) >> 4 : 32u >> 4, b_step = (16u * 128u) >> 4;
-        for (int kb = u.kb0; kb < u.kb1; ++kb) {
-          if (!mbar_wait_warp(&full_bar[stage], phase, &abort_sh, tmo)) {
-            if (issuer) give_up(3);
+        for (int r0 = u.kb0; ok && r0 < u.kb1; r0 += kRunKb) {
+          const int r1 = min(u.kb1, r0 + kRunKb);
+          if (!mbar_wait_warp(&acce_bar[acc], acc_phase ^ 1u, &abort_sh, tmo)) {
+            if (issuer) give_up(2);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + (size_t)stage * C::STAGE), b_addr = a_addr + C::A_BYTES;
-          const uint64_t ad0 = u.dw ? sdesc_sw128_mn(a_addr, C::RUN) : sdesc_sw128(a_addr);
-          const uint64_t bd0 = sdesc_sw128_mn(b_addr, C::RUN);
-          if (issuer) {
+          const uint32_t d_tmem = tmem + (uint32_t)(acc * BN);
+          for (int kb = r0; kb < r1; ++kb) {
+            if (!mbar_wait_warp(&full_bar[stage], phase, &abort_sh, tmo)) {
+              if (issuer) give_up(3);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a_addr = smem_u32(smem + (size_t)stage * C::STAGE), b_addr = a_addr + C::A_BYTES;
+            const uint64_t ad0 = u.dw ? sdesc_sw128_mn(a_addr, C::RUN) : sdesc_sw128(a_addr);
+            const uint64_t bd0 = sdesc_sw128_mn(b_addr, C::RUN);
+            if (issuer) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              tc_mma_pair<1>(d_tmem, ad0 + a_step * j, bd0 + b_step * j, idesc, (kb > u.kb0 || j > 0) ? 1u : 0u);
-            tc_commit_pair(&empty_bar[stage], (uint16_t)3);
+              for (int j = 0; j < 4; ++j)
+                tc_mma_pair<1>(d_tmem, ad0 + a_step * j, bd0 + b_step * j, idesc, (kb > r0 || j > 0) ? 1u : 0u);
+              tc_commit_pair(&empty_bar[stage], (uint16_t)3);
+            }
+            if (++stage == C::STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
+          if (!ok) break;
+          if (issuer) tc_commit_pair(&accf_bar[acc], (uint16_t)3);
+          if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1u;
           }
-        }
-        if (!ok) break;
-        if (issuer) tc_commit_pair(&accf_bar[acc], (uint16_t)3);
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
         }
       }
       if (issuer) tc_commit_pair(&drain_bar, (uint16_t)3);
@@ -459,51 +472,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     if (a.dbias)  // while the first tile is summed
       for (int c = ((int)blockIdx.x * kGradEpiWarps + ew) * 4; c < 2 * a.F; c += (int)gridDim.x * kGradEpiWarps * 4)
         dbias_columns(a.part, 2 * a.F, a.row_blocks, c, lane, a.dbias);
+    // this warp's columns of the runs so far, [WCOLS][32 lanes]: a thread reads back what it wrote
+    float* run = a.runs + ((size_t)(2 * pair + (int)rank) * kGradEpiWarps + ew) * (C::WCOLS * 32) + lane;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int i = 0; grad_unit(a, pair, pairs, i, BN, u); ++i) {
-      if (!mbar_wait_warp(&accf_bar[acc], acc_phase, &abort_sh, tmo)) {
-        if (lane == 0) give_up(4);
-        break;
-      }
-      tc_fence_after();
-      const int r0 = (int)rank * 128 + lq * 32, c0 = part * C::WCOLS;
-      const int row0 = u.m0 + r0, col0 = u.n0 + c0;
-      const int rows = min(32, (u.dw ? a.F : a.T) - row0);
-      uint8_t* out = static_cast<uint8_t*>(u.dw ? a.dW : a.dX) +
-                     ((int64_t)(u.dw ? u.z * a.F : 0) + row0) * a.k * 2;
-      float* fp32 = a.partial + ((size_t)max(u.slot, 0) * 256 + r0) * BN + c0;
-      const uint32_t taddr = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * BN + c0);
-#pragma unroll 1
-      for (int c = 0; c < C::WCOLS; c += 64) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float v[32];
-          __syncwarp();
-          tmem_ld32(taddr + (uint32_t)(c + 32 * h), *reinterpret_cast<uint32_t(*)[32]>(v));
-          tmem_wait_ld();
-          if (h == 1 && c + 64 == C::WCOLS) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(acce_lead0 + 8u * (uint32_t)acc);
-          }
-          if (u.slot >= 0) {
-            stage_row<OUT_F32, 128, 32>(buf, (uint32_t)lane, 0, v);
-            __syncwarp();
-            stage_flush<128, 4>(buf, reinterpret_cast<uint8_t*>(fp32 + c + 32 * h), (int64_t)BN * 4, 32, 128, true, lane);
-          } else {
-            stage_row<OT, 128, 32>(buf, (uint32_t)lane, (uint32_t)(4 * h), v);
-          }
+    bool ok = true;
+    for (int i = 0; ok && grad_unit(a, pair, pairs, i, BN, u); ++i) {
+      for (int k0 = u.kb0; k0 < u.kb1; k0 += kRunKb) {
+        const bool first = k0 == u.kb0, last = k0 + kRunKb >= u.kb1;
+        if (!mbar_wait_warp(&accf_bar[acc], acc_phase, &abort_sh, tmo)) {
+          if (lane == 0) give_up(4);
+          ok = false;
+          break;
         }
-        __syncwarp();
-        if (u.slot < 0 && rows > 0 && col0 + c < a.k)
-          stage_flush<128, 2>(buf, out + (int64_t)(col0 + c) * 2, (int64_t)a.k * 2, rows, min(64, a.k - col0 - c) * 2,
-                              true, lane);
-        __syncwarp();
-      }
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1u;
+        tc_fence_after();
+        const int r0 = (int)rank * 128 + lq * 32, c0 = part * C::WCOLS;
+        const int row0 = u.m0 + r0, col0 = u.n0 + c0;
+        const int rows = min(32, (u.dw ? a.F : a.T) - row0);
+        uint8_t* out = static_cast<uint8_t*>(u.dw ? a.dW : a.dX) +
+                       ((int64_t)(u.dw ? u.z * a.F : 0) + row0) * a.k * 2;
+        float* fp32 = a.partial + ((size_t)max(u.slot, 0) * 256 + r0) * BN + c0;
+        const uint32_t taddr = tmem + ((uint32_t)(lq * 32) << 16) + (uint32_t)(acc * BN + c0);
+#pragma unroll 1
+        for (int c = 0; c < C::WCOLS; c += 64) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v[32];
+            __syncwarp();
+            tmem_ld32(taddr + (uint32_t)(c + 32 * h), *reinterpret_cast<uint32_t(*)[32]>(v));
+            tmem_wait_ld();
+            if (h == 1 && c + 64 == C::WCOLS) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster_relaxed(acce_lead0 + 8u * (uint32_t)acc);
+            }
+            float* so_far = run + (c + 32 * h) * 32;
+            if (!first) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] += __ldcg(so_far + j * 32);
+            }
+            if (!last) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) __stcg(so_far + j * 32, v[j]);
+              continue;
+            }
+            if (u.slot >= 0) {
+              stage_row<OUT_F32, 128, 32>(buf, (uint32_t)lane, 0, v);
+              __syncwarp();
+              stage_flush<128, 4>(buf, reinterpret_cast<uint8_t*>(fp32 + c + 32 * h), (int64_t)BN * 4, 32, 128, true, lane);
+            } else {
+              stage_row<OT, 128, 32>(buf, (uint32_t)lane, (uint32_t)(4 * h), v);
+            }
+          }
+          __syncwarp();
+          if (last && u.slot < 0 && rows > 0 && col0 + c < a.k)
+            stage_flush<128, 2>(buf, out + (int64_t)(col0 + c) * 2, (int64_t)a.k * 2, rows, min(64, a.k - col0 - c) * 2,
+                                true, lane);
+          __syncwarp();
+        }
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
       }
     }
   }
@@ -673,10 +703,10 @@ int64_t plan_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw, int
   return cost;
 }
 
-// Workspace: dp, the masked dense weight, the row blocks' column sums, and partial
-// tiles of cut sums (one per pair at most).
+// Workspace: dp, the masked dense weight, the row blocks' column sums, partial tiles
+// of cut sums (one per pair at most), and a tile per pair for sums of several runs.
 struct GradWs {
-  int64_t pitch, dp, wm, part, partial, total;
+  int64_t pitch, dp, wm, part, partial, runs, total;
   GradWs(const nm_handle* h, int64_t T) {
     const int64_t F = h->n_out / 2, pairs = num_sms(h->device) / 2;
     pitch = (F + 63) / 64 * 64;  // whole 128-byte lines: a 128-byte box row then touches one
@@ -687,7 +717,9 @@ struct GradWs {
     partial = part + align256((T + rows - 1) / rows * h->n_out * 4);
     // with more 128-wide tiles than twice the pairs on both sides nothing is cut
     const int64_t n_nt = (h->k + 127) / 128, tiles = std::min(2 * ((F + 255) / 256), (T + 255) / 256) * n_nt;
-    total = partial + (tiles <= 2 * pairs ? pairs * 256 * 256 * 4 : 0);
+    const int64_t tile_bytes = pairs * 256 * 256 * 4, longest = std::max(T, 2 * ((F + kGradKb - 1) / kGradKb) * kGradKb);
+    runs = partial + (tiles <= 2 * pairs ? tile_bytes : 0);
+    total = runs + (longest > (int64_t)kRunKb * kGradKb ? tile_bytes : 0);
   }
 };
 
@@ -756,8 +788,7 @@ nm_status check_grad(const nm_handle* h, int64_t T) {
   if (!h->gated || h->mx) return fail(NM_ERR_INVALID, "nm_gated_backward needs a handle made by nm_compress_gated");
   if (h->dt == DT_I8) return fail(NM_ERR_UNSUPPORTED, "gradients are for FP16 and BF16 handles only");
   if (T < 0) return fail(NM_ERR_INVALID, "T must be >= 0 (got %lld)", (long long)T);
-  // a tile of dW sums over all of T in one go: 2^26 tokens take it a third of the
-  // second that its waits are bounded by
+  // tokens, row blocks and stages are counted in 32 bits, with room to spare
   if (T > (int64_t(1) << 26)) return fail(NM_ERR_UNSUPPORTED, "T above 2^26");
   return NM_OK;
 }
@@ -842,7 +873,7 @@ nm_status nm_gated_backward(const nm_handle* h, const void* X, const void* P, co
   GradArgs a{};
   int bn = 0, grid = 0;
   if ((dX || dW) && (st = choose_grad(h, T, dX != nullptr, dW != nullptr, &a, &grid, &bn)) != NM_OK) return st;
-  if ((a.side[0].splits > 1 || a.side[1].splits > 1) && lay.partial == lay.total)
+  if ((a.side[0].splits > 1 || a.side[1].splits > 1) && lay.partial == lay.runs)
     return fail(NM_ERR_INVALID, "the workspace has no room for partial tiles");
   cudaError_t e = cudaSuccess;
   const bool vec = F % 8 == 0;  // every row starts on 16 bytes
@@ -852,6 +883,7 @@ nm_status nm_gated_backward(const nm_handle* h, const void* X, const void* P, co
 
   if (dX || dW) {
     a.partial = reinterpret_cast<float*>(base + lay.partial);
+    a.runs = reinterpret_cast<float*>(base + lay.runs);
     a.dW = dW;
     a.dX = dX;
     a.part = part;
