@@ -334,6 +334,10 @@ nm_status nm_spmm_gated(const nm_handle* h, const void* X_dev, int64_t T, void* 
  * rounded to nearest.  With h half a unit of the handle's type (2^-11, 2^-8) and A
  * the sum of |dp| |Wm| (dW: |dp| |X|) over the n = 2 n_ff (dW: T) terms, a result r
  * is within (h + min(n, 2^14) 2^-26 + 2^-17 + n 2^-38) A + h |r| of the exact one.
+ * FP16: dp keeps the range of fp32, not fp16's.  Where the largest finite |dp| is
+ * outside [2^-4, 2^15) it is stored times a power of two, which the products undo
+ * (a second pass over P and dY); an element of dp is then off by h |dp| + 2^-21
+ * of the largest |dp| at most.
  *
  * dX_dev, dW_dev, dbias_dev: any may be NULL (not computed), not all three.
  * X_dev [T][k] (needed for dW only, else may be NULL), P_dev [T][2 n_ff],

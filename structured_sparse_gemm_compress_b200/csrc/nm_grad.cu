@@ -92,18 +92,57 @@ struct UnpackArgs {
   int img, n_kb, n_ff, blocks;
 };
 
+// dp of row t, this lane's eight columns from f0: g the gate half, u the up half.
+template <int DT, bool VEC>
+__device__ __forceinline__ void dp_row(const uint16_t* __restrict__ P, const uint16_t* __restrict__ dY, int t, int f0, int F,
+                                       int lane, int act, float (&g)[8], float (&u)[8]) {
+  const uint16_t* prow = P + (size_t)t * 2 * F;
+  float dy[8];
+  dp_load<DT, VEC>(prow, f0, F, lane, g);
+  dp_load<DT, VEC>(prow + F, f0, F, lane, u);
+  dp_load<DT, VEC>(dY + (size_t)t * F, f0, F, lane, dy);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float a, d;
+    act_slope(g[j], act, a, d);
+    g[j] = __fmul_rn(__fmul_rn(dy[j], u[j]), d);
+    u[j] = __fmul_rn(dy[j], a);
+  }
+}
+
+// Range of dp in fp16.  dY and u are fp16 values, their product is not: above 65504 it
+// would become infinite (and with a zero of the pruned weight NaN), below 2^-24 zero,
+// where fp32 keeps it and the sums it goes into may well be representable.  So each block
+// leaves its largest finite |dp|, and where the largest of all is outside [2^-4, 2^15)
+// gated_dp_scale_kernel writes dp again, times the power of two that brings it to [2^14,
+// 2^15); the products divide by it before they round.  An element is off by its rounding
+// and 2^-21 of the largest |dp| at most.  The whole call in graphs, before, in range and
+// outside it: 1379 x 768 -> 2 x 2051 30.3, 34.0, 39.7 us; 6304 x 1024 -> 2 x 4096 208,
+// 210, 262.  (A pass that only looks for the maximum first would cost the last figures
+// always; 148 blocks here instead of 592 the same in range, 322 outside.)
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+  const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+  return b < 0x7F800000u ? b : 0u;
+}
+// The power of two, as its exponent, that dp is stored times (0 without any finite non-zero).
+__device__ __forceinline__ int dp_exponent(uint32_t peak) {
+  const int e = (int)(peak >> 23) - 127;
+  return peak == 0u || (e >= -4 && e <= 14) ? 0 : min(14 - e, 126);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
 // One pass over P and dY: dp [T][2][pitch] in the handle's type (rounded for the
 // tensor core; columns n_ff .. pitch are never read) and, with `part`, the fp32
 // column sums of this block's rows ([row block][2][n_ff]), each warp's rows in
 // ascending order, the warps in order.  Memory bound: 48-51 us for 6304 x 2 x 4096
 // bf16 with the weight unpacked beside it (246 MB of DRAM traffic, 5 TB/s).
 // BIAS is its own instance: the sums' registers cost the plain one a third of its
-// warps.
+// warps.  With `peak` (fp16): this block's largest finite |dp|, as bits.
 template <int DT, bool VEC, bool BIAS>
 __global__ void __launch_bounds__(32 * kDpWarps, BIAS ? 3 : 4)
     gated_dp_kernel(const uint16_t* __restrict__ P, const uint16_t* __restrict__ dY, int T, int F, int pitch, int act,
-                    uint16_t* __restrict__ dp, float* __restrict__ part, int block_rows, int col_blocks,
-                    const UnpackArgs un) {
+                    uint16_t* __restrict__ dp, float* __restrict__ part, uint32_t* __restrict__ peak, int block_rows,
+                    int col_blocks, const UnpackArgs un) {
   __shared__ float sums[BIAS ? kDpWarps : 1][2][kDpCols];
   pdl_launch_dependents();
   pdl_wait();
@@ -120,26 +159,34 @@ __global__ void __launch_bounds__(32 * kDpWarps, BIAS ? 3 : 4)
   const int f0 = (block - row_block * col_blocks) * kDpCols, t0 = row_block * block_rows;
   const int t1 = min(T, t0 + block_rows);
   float sg[8] = {}, su[8] = {};
+  [[maybe_unused]] uint32_t top = 0;
   for (int t = t0 + warp; t < t1; t += kDpWarps) {
-    const uint16_t* prow = P + (size_t)t * 2 * F;
-    float g[8], u[8], dy[8];
-    dp_load<DT, VEC>(prow, f0, F, lane, g);
-    dp_load<DT, VEC>(prow + F, f0, F, lane, u);
-    dp_load<DT, VEC>(dY + (size_t)t * F, f0, F, lane, dy);
+    float g[8], u[8];
+    dp_row<DT, VEC>(P, dY, t, f0, F, lane, act, g, u);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float a, d;
-      act_slope(g[j], act, a, d);
-      g[j] = __fmul_rn(__fmul_rn(dy[j], u[j]), d);
-      u[j] = __fmul_rn(dy[j], a);
       if constexpr (BIAS) {
         sg[j] += g[j];
         su[j] += u[j];
       }
+      if constexpr (DT == DT_F16) top = max(top, max(finite_bits(g[j]), finite_bits(u[j])));
     }
     uint16_t* out = dp + (size_t)t * 2 * pitch;
     dp_store<DT, VEC>(out, f0, F, lane, g);
     dp_store<DT, VEC>(out + pitch, f0, F, lane, u);
+  }
+  if constexpr (DT == DT_F16) {
+    if (peak) {
+      __shared__ uint32_t tops[kDpWarps];
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) tops[warp] = top;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+#pragma unroll
+        for (int w = 1; w < kDpWarps; ++w) top = max(top, tops[w]);
+        peak[block] = top;
+      }
+    }
   }
   if constexpr (BIAS) {
 #pragma unroll
@@ -154,6 +201,46 @@ __global__ void __launch_bounds__(32 * kDpWarps, BIAS ? 3 : 4)
 #pragma unroll
       for (int w = 0; w < kDpWarps; ++w) s += sums[w][z][c];
       if (f0 + c < F) part[((size_t)row_block * 2 + z) * F + f0 + c] = s;
+    }
+  }
+}
+
+// fp16: decides from the blocks' largest |dp| whether dp has to be scaled, leaves the
+// factor that undoes it for the products, and if so writes dp again.
+template <bool VEC>
+__global__ void __launch_bounds__(32 * kDpWarps, 4)
+    gated_dp_scale_kernel(const uint16_t* __restrict__ P, const uint16_t* __restrict__ dY, int T, int F, int pitch, int act,
+                          uint16_t* __restrict__ dp, const uint32_t* peak, int blocks, int block_rows, int col_blocks,
+                          float* __restrict__ undo) {
+  __shared__ uint32_t tops[kDpWarps];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t top = 0;
+  for (int b = threadIdx.x; b < blocks; b += 32 * kDpWarps) top = max(top, __ldcg(peak + b));
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) tops[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kDpWarps; ++w) top = max(top, tops[w]);
+  const int e = dp_exponent(top);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *undo = pow2(-e);
+  if (e == 0) return;
+  const float scale = pow2(e);
+  for (int block = (int)blockIdx.x; block < blocks; block += (int)gridDim.x) {
+    const int row_block = block / col_blocks, f0 = (block - row_block * col_blocks) * kDpCols;
+    const int t0 = row_block * block_rows, t1 = min(T, t0 + block_rows);
+    for (int t = t0 + warp; t < t1; t += kDpWarps) {
+      float g[8], u[8];
+      dp_row<DT_F16, VEC>(P, dY, t, f0, F, lane, act, g, u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        g[j] *= scale;
+        u[j] *= scale;
+      }
+      uint16_t* out = dp + (size_t)t * 2 * pitch;
+      dp_store<DT_F16, VEC>(out, f0, F, lane, g);
+      dp_store<DT_F16, VEC>(out + pitch, f0, F, lane, u);
     }
   }
 }
@@ -254,6 +341,7 @@ struct GradArgs {
   float* partial;
   float* runs;             // sums of more than kRunKb stages: each epilogue warp's columns so far
   void *dW, *dX;
+  const float* undo;       // fp16: the factor that undoes dp's scaling
   const float* part;       // with dbias: the row blocks' column sums, row_blocks of them
   float* dbias;
   int row_blocks;
@@ -474,6 +562,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
         dbias_columns(a.part, 2 * a.F, a.row_blocks, c, lane, a.dbias);
     // this warp's columns of the runs so far, [WCOLS][32 lanes]: a thread reads back what it wrote
     float* run = a.runs + ((size_t)(2 * pair + (int)rank) * kGradEpiWarps + ew) * (C::WCOLS * 32) + lane;
+    [[maybe_unused]] float undo = 1.0f;
+    if constexpr (DT == DT_F16) undo = __ldcg(a.undo);
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
@@ -521,6 +611,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
               __syncwarp();
               stage_flush<128, 4>(buf, reinterpret_cast<uint8_t*>(fp32 + c + 32 * h), (int64_t)BN * 4, 32, 128, true, lane);
             } else {
+              if constexpr (DT == DT_F16) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= undo;
+              }
               stage_row<OT, 128, 32>(buf, (uint32_t)lane, (uint32_t)(4 * h), v);
             }
           }
@@ -563,6 +657,8 @@ __global__ void __launch_bounds__(256) grad_join_kernel(const GradArgs a) {
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), m = (g.dw ? mt % g.n_mt : mt) * 256 + row;
   if (m >= (g.dw ? a.F : a.T)) return;
   uint16_t* out = static_cast<uint16_t*>(g.dw ? a.dW : a.dX) + ((int64_t)(z * a.F) + m) * a.k;
+  [[maybe_unused]] float undo = 1.0f;
+  if constexpr (DT == DT_F16) undo = __ldcg(a.undo);
   for (int c = (threadIdx.x & 31) * 4; c < BN && nt * BN + c < a.k; c += 128) {
     const float* src = a.partial + ((size_t)first * 256 + row) * BN + c;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -573,6 +669,12 @@ __global__ void __launch_bounds__(256) grad_join_kernel(const GradArgs a) {
       v.y += w.y;
       v.z += w.z;
       v.w += w.w;
+    }
+    if constexpr (DT == DT_F16) {
+      v.x *= undo;
+      v.y *= undo;
+      v.z *= undo;
+      v.w *= undo;
     }
     *reinterpret_cast<uint2*>(out + nt * BN + c) = make_uint2(pack_pair<OT>(v.x, v.y), pack_pair<OT>(v.z, v.w));
   }
@@ -603,15 +705,22 @@ int dp_block_rows(int64_t T, int64_t F) {
 
 template <int DT>
 cudaError_t launch_dp(bool vec, const void* P, const void* dY, int T, int F, int pitch, int act, void* dp, float* part,
-                      const UnpackArgs& un, cudaStream_t s) {
+                      uint32_t* peak, float* undo, const UnpackArgs& un, int sms, cudaStream_t s) {
   const int rows = dp_block_rows(T, F), col_blocks = (F + kDpCols - 1) / kDpCols;
-  const int64_t blocks = (int64_t)((T + rows - 1) / rows) * col_blocks + un.blocks;
+  const int64_t blocks = (int64_t)((T + rows - 1) / rows) * col_blocks;
   const uint16_t *p = static_cast<const uint16_t*>(P), *y = static_cast<const uint16_t*>(dY);
   uint16_t* o = static_cast<uint16_t*>(dp);
   auto kern = vec ? (part ? gated_dp_kernel<DT, true, true> : gated_dp_kernel<DT, true, false>)
                   : (part ? gated_dp_kernel<DT, false, true> : gated_dp_kernel<DT, false, false>);
-  return launch_pdl(kern, dim3((unsigned)blocks), 32 * kDpWarps, 0, s, 0, p, y, T, F, pitch, act, o, part, rows, col_blocks,
-                    un);
+  cudaError_t e = launch_pdl(kern, dim3((unsigned)(blocks + un.blocks)), 32 * kDpWarps, 0, s, 0, p, y, T, F, pitch, act, o,
+                             part, peak, rows, col_blocks, un);
+  if constexpr (DT == DT_F16) {
+    if (e == cudaSuccess && peak)
+      e = launch_pdl(vec ? gated_dp_scale_kernel<true> : gated_dp_scale_kernel<false>,
+                     dim3((unsigned)std::min<int64_t>(blocks, 4 * sms)), 32 * kDpWarps, 0, s, 0, p, y, T, F, pitch, act, o,
+                     (const uint32_t*)peak, (int)blocks, rows, col_blocks, undo);
+  }
+  return e;
 }
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -703,10 +812,11 @@ int64_t plan_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw, int
   return cost;
 }
 
-// Workspace: dp, the masked dense weight, the row blocks' column sums, partial tiles
+// Workspace: dp, the masked dense weight, the row blocks' column sums, fp16: the factor
+// that undoes dp's scaling and the blocks' largest |dp|, partial tiles
 // of cut sums (one per pair at most), and a tile per pair for sums of several runs.
 struct GradWs {
-  int64_t pitch, dp, wm, part, partial, runs, total;
+  int64_t pitch, dp, wm, part, undo, peak, partial, runs, total;
   GradWs(const nm_handle* h, int64_t T) {
     const int64_t F = h->n_out / 2, pairs = num_sms(h->device) / 2;
     pitch = (F + 63) / 64 * 64;  // whole 128-byte lines: a 128-byte box row then touches one
@@ -714,7 +824,9 @@ struct GradWs {
     wm = dp + align256(T * 2 * pitch * 2);
     part = wm + align256(h->n_out * h->k * 2);
     const int64_t rows = dp_block_rows(T, F);
-    partial = part + align256((T + rows - 1) / rows * h->n_out * 4);
+    undo = part + align256((T + rows - 1) / rows * h->n_out * 4);
+    peak = undo + 256;
+    partial = h->dt == DT_F16 ? peak + align256((T + rows - 1) / rows * ((F + kDpCols - 1) / kDpCols) * 4) : undo;
     // with more 128-wide tiles than twice the pairs on both sides nothing is cut
     const int64_t n_nt = (h->k + 127) / 128, tiles = std::min(2 * ((F + 255) / 256), (T + 255) / 256) * n_nt;
     const int64_t tile_bytes = pairs * 256 * 256 * 4, longest = std::max(T, 2 * ((F + kGradKb - 1) / kGradKb) * kGradKb);
@@ -877,8 +989,12 @@ nm_status nm_gated_backward(const nm_handle* h, const void* X, const void* P, co
     return fail(NM_ERR_INVALID, "the workspace has no room for partial tiles");
   cudaError_t e = cudaSuccess;
   const bool vec = F % 8 == 0;  // every row starts on 16 bytes
-  e = h->dt == DT_F16 ? launch_dp<DT_F16>(vec, P, dY, (int)T, (int)F, (int)lay.pitch, (int)act, dp, part, un, s)
-                      : launch_dp<DT_BF16>(vec, P, dY, (int)T, (int)F, (int)lay.pitch, (int)act, dp, part, un, s);
+  float* undo = reinterpret_cast<float*>(base + lay.undo);
+  uint32_t* peak = h->dt == DT_F16 && (dX || dW) ? reinterpret_cast<uint32_t*>(base + lay.peak) : nullptr;
+  const int sms = num_sms(h->device);
+  e = h->dt == DT_F16
+          ? launch_dp<DT_F16>(vec, P, dY, (int)T, (int)F, (int)lay.pitch, (int)act, dp, part, peak, undo, un, sms, s)
+          : launch_dp<DT_BF16>(vec, P, dY, (int)T, (int)F, (int)lay.pitch, (int)act, dp, part, peak, undo, un, sms, s);
   if (e != cudaSuccess) return cuda_fail(e, "launch the gradient of the output stage");
 
   if (dX || dW) {
@@ -886,6 +1002,7 @@ nm_status nm_gated_backward(const nm_handle* h, const void* X, const void* P, co
     a.runs = reinterpret_cast<float*>(base + lay.runs);
     a.dW = dW;
     a.dX = dX;
+    a.undo = undo;
     a.part = part;
     a.dbias = dbias;
     a.row_blocks = row_blocks;

@@ -9,11 +9,16 @@ bounds (2^-23, truncated) and as much again for the alignment within the step: n
 2^-23 = n 2^-26; the fp32 additions of the runs and of at most 74 parts of a cut sum
 round to nearest, n 2^-14 2^-24 and 74 x 2^-24 < 2^-17.  Where the inputs make dp exact
 in the handle's type, the first h is left out here.
+
+FP16: dp is stored times a power of two where its largest magnitude m is outside [2^-4,
+2^15).  Within, an element below fp16's normal range is off by 2^-25 <= 2^-21 m; scaled
+to m in [2^14, 2^15) by 2^-39 m: h |dp| + 2^-21 m covers both.
 """
 import pytest
 import torch
 
 import structured_sparse_gemm_compress_b200 as nm
+from test_gpu_gated import dp_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +124,96 @@ def test_dp_is_rounded_once_and_nothing_else(dt, T, k, F):
     dp = (torch.cat((P[:, F:], P[:, :F]), dim=1).float() * dY.float().repeat(1, 2)).to(DTS[dt])
     close(dX, dp, Wm, 2 * F)
     close(dW, dp.t(), X, T)
+
+
+# ------------------------------------------------------------------ fp16: dp beyond fp16's range
+
+def fp16_case(T, k, F, scales, act, seed=0, spike=None):
+    """X, P, dY, W of normal values times `scales`; spike: one entry of dY times that."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    X, P, dY, W = ((torch.randn(s, generator=g, device="cuda") * c).half()
+                   for s, c in zip(((T, k), (T, 2 * F), (T, F), (2 * F, k)), scales))
+    if spike:
+        dY[T // 2, F // 3] *= spike
+    return X, P, dY, W
+
+
+def check_range(T, k, F, scales, act="none", N=2, M=4, seed=0, spike=None):
+    X, P, dY, W = fp16_case(T, k, F, scales, act, seed, spike)
+    h = nm.nm_compress_gated(W, N, M)
+    dX, dW, db = backward(h, X, P, dY, act)
+    dp, e = dp_reference(P, dY, act)
+    dp, e = torch.from_numpy(dp).cuda(), torch.from_numpy(e).cuda()
+    # the header's error of an element of dp, and what the activation adds
+    e = e + 2.0 ** -11 * (dp.abs() + e) + 2.0 ** -21 * float(dp.abs().max())
+    assert torch.isfinite(dX).all() and torch.isfinite(dW).all()
+    close(dX, dp, nm.nm_decompress(h), 2 * F, e)
+    close(dW, dp.t(), X, T, e.t())
+    return dp, dX, dW
+
+
+@pytest.mark.parametrize("T,k,F", [(1, 64, 24), (65, 128, 64), (200, 264, 1030), (3000, 64, 40), (333, 520, 129)])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu", "relu"])
+@pytest.mark.parametrize("scales", [(2.0 ** -9, 300.0, 300.0, 2.0 ** -9),     # |dp| up to a million and more
+                                    (100.0, 2.0 ** -10, 2.0 ** -14, 3.0),    # |dp| around 2^-24, dX and dW not
+                                    (1.0, 1.0, 2.0 ** -12, 1.0)])            # gradients of a mean: below fp16's normal range
+def test_dp_beyond_the_range_of_fp16(T, k, F, act, scales):
+    check_range(T, k, F, scales, act, seed=T)
+
+
+@pytest.mark.parametrize("F", [40, 41])
+def test_one_large_dp_among_ordinary_ones(F):
+    dp, _, _ = check_range(100, 64, F, (2.0 ** -6, 30.0, 1.0, 2.0 ** -8), spike=2.0 ** 13, seed=3)
+    assert float(dp.abs().max()) > 65504
+
+
+@pytest.mark.parametrize("F", [1, 8])
+def test_powers_of_two_come_out_exactly(F):
+    """A single dp of 2^s: both sides of every border of the range, to the bit."""
+    for s in range(-29, 30):
+        w = min(max(-s, -14), 15)
+        X = torch.full((1, 8), 2.0 ** w, device="cuda").half()
+        W = torch.zeros((2 * F, 8), device="cuda").half()
+        W[0] = 2.0 ** w
+        P, dY = torch.zeros((1, 2 * F), device="cuda").half(), torch.zeros((1, F), device="cuda").half()
+        P[0, F], dY[0, 0] = 2.0 ** (s // 2), 2.0 ** (s - s // 2)
+        dX, dW, db = backward(nm.nm_compress_gated(W, 4, 4), X, P, dY, "none")
+        assert bool((dX == 2.0 ** (s + w)).all()) and bool((dW[0] == 2.0 ** (s + w)).all()), s
+        assert not dW[1:].any() and float(db[0]) == 2.0 ** s
+
+
+def test_nothing_and_infinities_in_dp():
+    T, k, F = 90, 64, 48
+    X, P, dY, W = fp16_case(T, k, F, (1.0, 1.0, 2.0 ** -13, 1.0), "none")
+    h = nm.nm_compress_gated(W, 2, 4)
+    dX, dW, db = backward(h, X, P, torch.zeros_like(dY), "none")
+    assert not dX.any() and not dW.any() and not db.any()
+    # an infinity spoils its token and its two channels, and the others keep their range
+    P[7, 5] = P[7, F + 5] = 1.0
+    dY[7, 5] = 0.0
+    clean = backward(h, X, P, dY, "none")
+    dY[7, 5] = float("inf")
+    dX, dW, _ = backward(h, X, P, dY, "none")
+    rows, cols = [t for t in range(T) if t != 7], [f for f in range(2 * F) if f % F != 5]
+    assert torch.equal(dX[rows], clean[0][rows]) and torch.equal(dW[cols], clean[1][cols])
+    assert not torch.isfinite(dX[7]).any() and not torch.isfinite(dW[[5, F + 5]]).any()
+
+
+def test_range_is_decided_in_the_captured_call():
+    T, k, F = 150, 128, 80
+    sets = [fp16_case(T, k, F, s, "silu", seed=i) for i, s in enumerate((
+        (1.0, 1.0, 1.0, 1.0), (2.0 ** -9, 300.0, 300.0, 1.0), (1.0, 1.0, 2.0 ** -14, 1.0)))]
+    W = sets[0][3] * 2.0 ** -6
+    h = nm.nm_compress_gated(W, 2, 4)
+    want = [nm.nm_gated_backward(h, *s[:3], bias_grad=True) for s in sets]
+    held = [t.clone() for t in sets[0][:3]]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = nm.nm_gated_backward(h, *held, bias_grad=True)
+    for i in (0, 1, 2, 1, 0):
+        for a, b in zip(held, sets[i]):
+            a.copy_(b)
+        graph.replay()
+        for a, b in zip(out, want[i]):
+            assert torch.equal(a, b)
