@@ -300,11 +300,12 @@ nm_status nm_compress_gated(const void* W_dev, int64_t n_ff, int64_t k, nm_dtype
  *   p[t][r] = acc(X . Wm^T)[t][r] * scale[r] + bias[r]      r in [0, 2 n_ff)
  *   Y[t][f] = act(p[t][f]) * p[t][n_ff + f]                 f in [0, n_ff)
  * with acc the accumulator of nm_spmm, in fp32, each step rounded to nearest as in
- * nm_spmm_ex, Y rounded once to its type.  act is any nm_act.  ep->scale and ep->bias are [2 n_ff] (or NULL);
- * output types, errors and defaults are nm_spmm_ex's, but NM_OUT_INT32 is
- * refused, and the default of an INT8 handle is fp32.  ep == NULL: NM_ACT_SILU,
- * default output.  The SiLU is within (6e-7 + 1.3e-7 max(0, -v)) |SiLU(v)| +
- * 1e-36 of the exact one.
+ * nm_spmm_ex, Y rounded once to its type.  act is any nm_act.  ep->scale and
+ * ep->bias are [2 n_ff] (or NULL); output types, errors and defaults are
+ * nm_spmm_ex's, but NM_OUT_INT32 is refused, and the default of an INT8 handle is
+ * fp32.  ep == NULL: NM_ACT_SILU, default output.  The SiLU is within
+ * (6e-7 + 1.3e-7 max(0, -v)) |SiLU(v)| + 1.1e-36 of the exact one (below -87.33,
+ * where the reciprocal of 1 + exp(-v) is subnormal, it is -0).
  *
  * P_dev, if not NULL, receives p itself, [T][2 n_ff] in the handle's type
  * (FP16/BF16; an INT8 handle refuses it with NM_ERR_UNSUPPORTED): what
