@@ -46,14 +46,15 @@ def _compile(src: str, force: bool, extra: list[str], objdir: str = OBJDIR) -> s
 
 
 def _binding(force: bool) -> str:
-    """_binding.so: csrc/nm_binding.cpp against torch's C++ library (rebuilt for another torch)."""
+    """_binding.so: csrc/nm_binding.cpp against torch's C++ library (rebuilt for another torch or Python)."""
     import sysconfig
 
     import torch
 
     src, stamp = os.path.join(CSRC, "nm_binding.cpp"), os.path.join(OBJDIR, "binding.torch")
     built_for = open(stamp).read() if os.path.exists(stamp) else ""
-    if force or _stale(BINDING, src) or built_for != torch.__version__:
+    wanted = f"{torch.__version__} {sysconfig.get_config_var('SOABI')}"
+    if force or _stale(BINDING, src) or built_for != wanted:
         root = os.path.dirname(torch.__file__)
         dirs = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                 os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), sysconfig.get_paths()["include"]]
@@ -65,7 +66,7 @@ def _binding(force: bool) -> str:
                                "-ltorch_cuda", "-lc10", "-lc10_cuda"])
         os.replace(tmp, BINDING)
         with open(stamp, "w") as f:
-            f.write(torch.__version__)
+            f.write(wanted)
     return BINDING
 
 
@@ -78,13 +79,14 @@ def build(force: bool = False, verbose_ptxas: bool = False, trace: bool = False)
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = None if trace else ex.submit(_binding, force)
         objs = list(ex.map(lambda s: _compile(s, force, extra, objdir), SOURCES))
-        if binding is not None:
-            binding.result()
     if force or not os.path.exists(lib) or any(os.path.getmtime(o) > os.path.getmtime(lib) for o in objs):
         tmp = lib + f".{os.getpid()}.tmp"
         subprocess.check_call([NVCC, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", *objs,
                                "-o", tmp, "-lcudart"])
         os.replace(tmp, lib)
+    if binding is not None and binding.exception() is not None:  # the C library needs none of it: it is there
+        raise RuntimeError(f"{lib} is built, but not the Python binding, which needs {CXX} and torch's "
+                           f"headers: {binding.exception()}") from binding.exception()
     return lib
 
 
