@@ -119,7 +119,7 @@ __device__ __forceinline__ void dp_row(const uint16_t* __restrict__ P, const uin
 // and 2^-21 of the largest |dp| at most.  The whole call in graphs, before, in range and
 // outside it: 1379 x 768 -> 2 x 2051 30.3, 34.0, 39.7 us; 6304 x 1024 -> 2 x 4096 208,
 // 210, 262.  (A pass that only looks for the maximum first would cost the last figures
-// always; 148 blocks here instead of 592 the same in range, 322 outside.)
+// always; one block an SM here instead of four the same in range, 322 outside.)
 __device__ __forceinline__ uint32_t finite_bits(float x) {
   const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
   return b < 0x7F800000u ? b : 0u;
@@ -698,15 +698,15 @@ cudaError_t launch_grad_t(int grid, const GradMaps& m, const GradArgs& a, cudaSt
 
 // Rows per block: eight a warp, or two when that would leave SMs without a block
 // (1379 x 2 x 2051 with the bias: 18.6 us with 16 rows a warp, 11.1 with two).
-int dp_block_rows(int64_t T, int64_t F) {
+int dp_block_rows(int64_t T, int64_t F, int sms) {
   const int64_t col_blocks = (F + kDpCols - 1) / kDpCols;
-  return (T + 63) / 64 * col_blocks >= 4 * 148 ? 64 : 16;
+  return (T + 63) / 64 * col_blocks >= 4 * sms ? 64 : 16;
 }
 
 template <int DT>
 cudaError_t launch_dp(bool vec, const void* P, const void* dY, int T, int F, int pitch, int act, void* dp, float* part,
                       uint32_t* peak, float* undo, const UnpackArgs& un, int sms, cudaStream_t s) {
-  const int rows = dp_block_rows(T, F), col_blocks = (F + kDpCols - 1) / kDpCols;
+  const int rows = dp_block_rows(T, F, sms), col_blocks = (F + kDpCols - 1) / kDpCols;
   const int64_t blocks = (int64_t)((T + rows - 1) / rows) * col_blocks;
   const uint16_t *p = static_cast<const uint16_t*>(P), *y = static_cast<const uint16_t*>(dY);
   uint16_t* o = static_cast<uint16_t*>(dp);
@@ -818,12 +818,13 @@ int64_t plan_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw, int
 struct GradWs {
   int64_t pitch, dp, wm, part, undo, peak, partial, runs, total;
   GradWs(const nm_handle* h, int64_t T) {
-    const int64_t F = h->n_out / 2, pairs = num_sms(h->device) / 2;
+    const int sms = num_sms(h->device);
+    const int64_t F = h->n_out / 2, pairs = sms / 2;
     pitch = (F + 63) / 64 * 64;  // whole 128-byte lines: a 128-byte box row then touches one
     dp = 0;
     wm = dp + align256(T * 2 * pitch * 2);
     part = wm + align256(h->n_out * h->k * 2);
-    const int64_t rows = dp_block_rows(T, F);
+    const int64_t rows = dp_block_rows(T, F, sms);
     undo = part + align256((T + rows - 1) / rows * h->n_out * 4);
     peak = undo + 256;
     partial = h->dt == DT_F16 ? peak + align256((T + rows - 1) / rows * ((F + kDpCols - 1) / kDpCols) * 4) : undo;
@@ -968,7 +969,7 @@ nm_status nm_gated_backward(const nm_handle* h, const void* X, const void* P, co
   uint8_t* base = static_cast<uint8_t*>(ws);
   void* dp = base + lay.dp;
   float* part = dbias ? reinterpret_cast<float*>(base + lay.part) : nullptr;
-  const int rows = dp_block_rows(T, F), row_blocks = (int)((T + rows - 1) / rows);
+  const int sms = num_sms(h->device), rows = dp_block_rows(T, F, sms), row_blocks = (int)((T + rows - 1) / rows);
   UnpackArgs un{};
   if (dX) {
     un.bpack = h->d_bpack;
@@ -991,7 +992,6 @@ nm_status nm_gated_backward(const nm_handle* h, const void* X, const void* P, co
   const bool vec = F % 8 == 0;  // every row starts on 16 bytes
   float* undo = reinterpret_cast<float*>(base + lay.undo);
   uint32_t* peak = h->dt == DT_F16 && (dX || dW) ? reinterpret_cast<uint32_t*>(base + lay.peak) : nullptr;
-  const int sms = num_sms(h->device);
   e = h->dt == DT_F16
           ? launch_dp<DT_F16>(vec, P, dY, (int)T, (int)F, (int)lay.pitch, (int)act, dp, part, peak, undo, un, sms, s)
           : launch_dp<DT_BF16>(vec, P, dY, (int)T, (int)F, (int)lay.pitch, (int)act, dp, part, peak, undo, un, sms, s);

@@ -263,11 +263,11 @@ cudaError_t launch_quantize_dt(int dt, int N, int M, const void* X, int64_t rows
 
 template <int DT>
 cudaError_t launch_dequantize(const uint8_t* Q, const uint8_t* S, int64_t rows, int64_t k, int64_t n_ff, void* X,
-                              cudaStream_t s) {
+                              int sms, cudaStream_t s) {
   const int64_t units = k * src_bytes(DT) / 16;  // of a row
   const int cols = (int)(units < 2048 ? units : 2048);
   // as many blocks as are resident at once (8 an SM), of 256 units at least
-  const int64_t chunks = (units + cols - 1) / cols, want = (rows * chunks + 8 * 148 - 1) / (8 * 148);
+  const int64_t chunks = (units + cols - 1) / cols, want = (rows * chunks + 8 * sms - 1) / (8 * sms);
   const int block_rows = (int)(want * cols > 256 ? want : (256 + cols - 1) / cols);
   const dim3 grid((unsigned)((rows + block_rows - 1) / block_rows), (unsigned)((units + cols - 1) / cols));
   return launch_pdl(mx_dequantize_kernel<DT>, grid, 256, 0, s, 0, Q, S, rows, k, n_ff, (k + 255) / 256, block_rows, cols,
@@ -839,7 +839,8 @@ cudaError_t launch_mx_pack(const nm_handle* h, const void* W, cudaStream_t s) {
 }
 
 cudaError_t launch_mx_unpack(const nm_handle* h, void* W, cudaStream_t s) {
-  return launch_dequantize<SRC_BF16>(h->d_mxq, h->d_mxs, h->mx_rows, h->k, h->gated ? h->n_out / 2 : 0, W, s);
+  return launch_dequantize<SRC_BF16>(h->d_mxq, h->d_mxs, h->mx_rows, h->k, h->gated ? h->n_out / 2 : 0, W,
+                                     num_sms(h->device), s);
 }
 
 }  // namespace nm
@@ -896,9 +897,13 @@ nm_status nm_mx_dequantize(const void* Q, const void* S, int64_t T, int64_t k, n
   if (overlaps(X, xbytes, Q, (size_t)T * (k / 2)) || overlaps(X, xbytes, S, (size_t)scale_bytes(T, k)))
     return fail(NM_ERR_INVALID, "X overlaps Q or S");
   const uint8_t *q = static_cast<const uint8_t*>(Q), *s = static_cast<const uint8_t*>(S);
-  cudaError_t e = dt == NM_FP32   ? launch_dequantize<SRC_F32>(q, s, T, k, 0, X, (cudaStream_t)stream)
-                  : dt == NM_FP16 ? launch_dequantize<SRC_F16>(q, s, T, k, 0, X, (cudaStream_t)stream)
-                                  : launch_dequantize<SRC_BF16>(q, s, T, k, 0, X, (cudaStream_t)stream);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "query the current device");
+  const int sms = num_sms(dev);
+  e = dt == NM_FP32   ? launch_dequantize<SRC_F32>(q, s, T, k, 0, X, sms, (cudaStream_t)stream)
+      : dt == NM_FP16 ? launch_dequantize<SRC_F16>(q, s, T, k, 0, X, sms, (cudaStream_t)stream)
+                      : launch_dequantize<SRC_BF16>(q, s, T, k, 0, X, sms, (cudaStream_t)stream);
   return e == cudaSuccess ? NM_OK : cuda_fail(e, "launch the dequantisation");
 }
 
