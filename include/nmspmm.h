@@ -140,7 +140,8 @@ nm_status nm_recompress(nm_handle* h, const void* W_dev, void* stream);
  *                                       sum |x| |w| of the exact sum.
  *           Must be 16-byte aligned and must not overlap X.
  * scale_dev float32 [n_out] or NULL.
- * T         >= 0; T == 0 is a no-op returning NM_OK.
+ * T         in [0, 2^31 - 256] (above: NM_ERR_UNSUPPORTED); T == 0 is a no-op
+ *           returning NM_OK.
  * The kernel, token tile and split-K factor are chosen per (T, k, n_out,
  * N:M, dtype) so that small token counts still occupy the SMs (section 4.1,
  * mechanism 3; nm_plan_query reports the choice).  A split chosen by the
@@ -260,7 +261,7 @@ nm_status nm_compress_tile(const void* W_dev, int64_t n_out, int64_t k, nm_dtype
  *           rounding exactly as nm_spmm (INT8: int32, or float32 with scale;
  *           FP16: fp16 from the fp32 accumulator).
  * scale_dev float32 [n_out] or NULL.
- * T         >= 0; T == 0 is a no-op.
+ * T         in [0, 2^31 - 256] (above: NM_ERR_UNSUPPORTED); T == 0 is a no-op.
  * The default plan never splits k, so the call allocates nothing and never
  * synchronises; a split-K plan forced through NMSPMM_FORCE_SPLITK reduces in
  * global memory and uses the handle's workspace under the rules of nm_spmm

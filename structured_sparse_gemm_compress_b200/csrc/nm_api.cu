@@ -253,6 +253,9 @@ bool make_y_map(nm_handle* h, void* Y, int64_t T, int out_es, int out_ty, int ch
   return true;
 }
 
+// The kernels count tokens in 32 bits, up to the end of the last tile (256 at most).
+constexpr int64_t kMaxTokens = INT32_MAX - 255;
+
 // Output element type and size of a launch: int32 / fp32 for INT8 (without /
 // with scale), else the input's 16-bit type.
 void out_type(const nm_handle* h, bool scaled, int* es, int* ty) {
@@ -656,7 +659,7 @@ nm_status spmm_impl(const nm_handle* hc, const void* X, int64_t T, void* Y, cons
   if (T < 0) return fail(NM_ERR_INVALID, "T must be >= 0 (got %lld)", (long long)T);
   if (T == 0) return NM_OK;
   if (!X || !Y) return fail(NM_ERR_INVALID, "null X or Y");
-  if (T > INT32_MAX) return fail(NM_ERR_UNSUPPORTED, "T above 2^31-1");
+  if (T > kMaxTokens) return fail(NM_ERR_UNSUPPORTED, "T above 2^31-256");
   const int es = nm::elem_bytes(h->dt);
   if (!aligned(X, 16) || !aligned(Y, 16)) return fail(NM_ERR_INVALID, "X and Y must be 16-byte aligned");
   if ((h->k * es) % 16 != 0)
@@ -829,8 +832,7 @@ nm_status nm_spmm_gated(const nm_handle* h, const void* X, int64_t T, void* Y, v
   if (T < 0) return fail(NM_ERR_INVALID, "T must be >= 0 (got %lld)", (long long)T);
   if (T == 0) return NM_OK;
   if (!X || !Y) return fail(NM_ERR_INVALID, "null X or Y");
-  if (T > INT32_MAX - 255)  // a tile's last token is counted in 32 bits
-    return fail(NM_ERR_UNSUPPORTED, "T above 2^31-256");
+  if (T > kMaxTokens) return fail(NM_ERR_UNSUPPORTED, "T above 2^31-256");
   const int es = nm::elem_bytes(h->dt);
   if (!aligned(X, 16) || !aligned(Y, 16) || !aligned(P, 16))
     return fail(NM_ERR_INVALID, "X, Y and P must be 16-byte aligned");
@@ -1076,7 +1078,7 @@ nm_status gather_impl(const nm_handle* hc, const void* Xt, int64_t ldx, int64_t 
   if (T < 0) return fail(NM_ERR_INVALID, "T must be >= 0 (got %lld)", (long long)T);
   if (T == 0) return NM_OK;
   if (!Xt || !Y) return fail(NM_ERR_INVALID, "null Xt or Y");
-  if (T > INT32_MAX) return fail(NM_ERR_UNSUPPORTED, "T above 2^31-1");
+  if (T > kMaxTokens) return fail(NM_ERR_UNSUPPORTED, "T above 2^31-256");
   const int es = nm::elem_bytes(h->dt);
   if (ldx < T) return fail(NM_ERR_INVALID, "ldx=%lld is below T=%lld", (long long)ldx, (long long)T);
   if ((ldx * es) % 16 != 0)
