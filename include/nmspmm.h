@@ -355,6 +355,24 @@ nm_status nm_gated_backward(const nm_handle* h, const void* X_dev, const void* P
                             void* stream);
 
 /*
+ * nm_gated_backward_plan_for_shape -- test and diagnostic hook: how
+ * nm_gated_backward would share out the two products of this shape (those asked
+ * for) over a GPU with `sms` SMs.  Touches no device.  The environment overrides
+ * NMSPMM_FORCE_GRAD_BN and NMSPMM_GRAD_SPLIT apply.  Errors: NM_ERR_INVALID for a
+ * null pointer or a bad shape, NM_ERR_UNSUPPORTED for one beyond the call's limits.
+ */
+typedef struct nm_grad_plan_info {
+  int bn;                    /* columns of a tile (256 rows) */
+  int grid;                  /* CTA pairs launched */
+  int splits_dx, splits_dw;  /* parts of a tile's sum (1: whole, 0: not asked for) */
+  int runs_dx, runs_dw;      /* accumulator runs of a part */
+  int64_t stages;            /* 64-deep stages of the fullest pair */
+  int complete;              /* 1: every stage of every tile is one pair's, every part has its slot */
+} nm_grad_plan_info;
+nm_status nm_gated_backward_plan_for_shape(int64_t n_ff, int64_t k, int64_t T, int want_dx, int want_dw, int sms,
+                                           nm_grad_plan_info* out);
+
+/*
  * Microscaled 4-bit floating point (the MXFP4 format of the OCP Microscaling
  * Formats specification, version 1.0).  (No counterpart in the paper: it is a
  * further storage format for the same linears.)  Along k, every block of 32

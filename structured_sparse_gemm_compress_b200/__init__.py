@@ -31,13 +31,20 @@ EXPORTS = ("nm_compress", "nm_compress_tile", "nm_recompress", "nm_spmm", "nm_sp
            "nm_plan_query", "nm_plan_for_shape", "nm_device_status", "nm_destroy", "nm_last_error", "nm_version",
            "nm_test_spmm_skip_stage", "nm_mx_scale_bytes", "nm_mx_quantize", "nm_mx_dequantize", "nm_compress_mx",
            "nm_spmm_mx", "nm_spmm_mx_gated", "nm_compress_gated", "nm_spmm_gated", "nm_gated_backward",
-           "nm_gated_backward_workspace")
+           "nm_gated_backward_workspace", "nm_gated_backward_plan_for_shape")
 
 
 class NMPlanInfo(ctypes.Structure):
     """nm_plan_info of include/nmspmm.h."""
     _fields_ = [("pair", ctypes.c_int), ("bn", ctypes.c_int), ("splits", ctypes.c_int),
                 ("cluster", ctypes.c_int), ("grid", ctypes.c_int), ("units", ctypes.c_int)]
+
+
+class NMGradPlanInfo(ctypes.Structure):
+    """nm_grad_plan_info of include/nmspmm.h."""
+    _fields_ = [("bn", ctypes.c_int), ("grid", ctypes.c_int), ("splits_dx", ctypes.c_int), ("splits_dw", ctypes.c_int),
+                ("runs_dx", ctypes.c_int), ("runs_dw", ctypes.c_int), ("stages", ctypes.c_int64),
+                ("complete", ctypes.c_int)]
 
 
 class NMError(RuntimeError):
@@ -85,6 +92,7 @@ def lib() -> ctypes.CDLL:
         L.nm_spmm_gated.argtypes = [vp, vp, i64, vp, vp, ctypes.POINTER(NMEpilogue), vp]
         L.nm_gated_backward_workspace.argtypes = [vp, i64, ctypes.POINTER(ctypes.c_size_t)]
         L.nm_gated_backward.argtypes = [vp, vp, vp, vp, i64, i32, vp, vp, vp, vp, ctypes.c_size_t, vp]
+        L.nm_gated_backward_plan_for_shape.argtypes = [i64, i64, i64, i32, i32, i32, ctypes.POINTER(NMGradPlanInfo)]
         L.nm_device_status.argtypes = [vp]
         L.nm_destroy.argtypes = [vp]
         L.nm_destroy.restype = None
@@ -95,7 +103,8 @@ def lib() -> ctypes.CDLL:
                      "nm_test_spmm_skip_stage", "nm_decompress", "nm_export", "nm_export_sizes", "nm_query",
                      "nm_plan_query", "nm_plan_for_shape", "nm_device_status", "nm_mx_scale_bytes", "nm_mx_quantize",
                      "nm_mx_dequantize", "nm_compress_mx", "nm_spmm_mx", "nm_spmm_mx_gated",
-                     "nm_compress_gated", "nm_spmm_gated", "nm_gated_backward", "nm_gated_backward_workspace"):
+                     "nm_compress_gated", "nm_spmm_gated", "nm_gated_backward", "nm_gated_backward_workspace",
+                     "nm_gated_backward_plan_for_shape"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -384,6 +393,15 @@ def nm_gated_backward(h: NMHandle, X: torch.Tensor, P: torch.Tensor, dY: torch.T
         raise ValueError(f"act must be one of {tuple(ACTS)}")
     return (_module or _native()).gated_backward(h.raw.value, h.n_out, h.k, h.dt, X, P, dY, ACTS[act], int(bias_grad), dX,
                                                  dW, dbias, workspace, stream)
+
+
+def nm_gated_backward_plan_for_shape(n_ff: int, k: int, T: int, sms: int, dx: bool = True, dw: bool = True) -> dict:
+    """How ``nm_gated_backward`` would share out its products on a GPU with ``sms`` SMs.  Needs
+    no GPU: a test and diagnostic hook."""
+    info = NMGradPlanInfo()
+    _check(lib().nm_gated_backward_plan_for_shape(int(n_ff), int(k), int(T), int(bool(dx)), int(bool(dw)), int(sms),
+                                                  ctypes.byref(info)))
+    return {f: getattr(info, f) for f, _ in NMGradPlanInfo._fields_}
 
 
 def nm_mx_scale_bytes(rows: int, k: int) -> int:

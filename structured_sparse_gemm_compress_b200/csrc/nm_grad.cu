@@ -359,7 +359,7 @@ struct GradUnit {
 // the pairs; `hi` pairs get one more of them than the others.  Side 1's: first
 // lo_units - hi_units rounds over the other pairs alone, then hi_units rounds
 // over all (hi_units <= lo_units), the last round cut off at the end of the list.
-__device__ __forceinline__ bool grad_unit(const GradArgs& a, int pair, int pairs, int i, int bn, GradUnit& u) {
+__host__ __device__ __forceinline__ bool grad_unit(const GradArgs& a, int pair, int pairs, int i, int bn, GradUnit& u) {
   const int n0 = a.side[0].tiles * a.side[0].splits;
   const int q = n0 / pairs + (pair < a.hi ? 1 : 0);
   int s = 0, unit;
@@ -388,7 +388,7 @@ __device__ __forceinline__ bool grad_unit(const GradArgs& a, int pair, int pairs
   const int nt = tile % g.n_nt, mt = tile / g.n_nt;
   u.dw = g.dw;
   u.kb0 = part * g.per_split;
-  u.kb1 = min(g.n_kb, u.kb0 + g.per_split);
+  u.kb1 = u.kb0 + g.per_split < g.n_kb ? u.kb0 + g.per_split : g.n_kb;
   u.slot = g.splits > 1 ? g.slot0 + unit : -1;
   u.n0 = nt * bn;
   u.z = g.dw ? mt / g.n_mt : 0;
@@ -757,13 +757,12 @@ int64_t share_out(const GradSide& x, const GradSide& y, int pairs, GradArgs* a, 
 
 // The launch for tiles bn columns wide: its stages (share_out), or -1 when there
 // are too many tiles.
-int64_t plan_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw, int bn, int pairs, bool may_cut, GradArgs* a,
-                  int* grid) {
-  const int64_t F = h->n_out / 2;
-  const int n_nt = (int)((h->k + bn - 1) / bn);
+int64_t plan_grad(int64_t F, int64_t k, int64_t T, bool want_dx, bool want_dw, int bn, int pairs, bool may_cut,
+                  GradArgs* a, int* grid) {
+  const int n_nt = (int)((k + bn - 1) / bn);
   a->F = (int)F;
   a->T = (int)T;
-  a->k = (int)h->k;
+  a->k = (int)k;
   a->kb_half = (int)((F + kGradKb - 1) / kGradKb);
   GradSide sw{}, sx{};
   sw.dw = 1;
@@ -847,12 +846,13 @@ int forced_grad_bn() {  // tests and sweeps
 // narrower tile moves 24 KB a stage and SM against 32 KB for half the products).
 // The choice is a function of the shape alone; a thread's last one is kept, since a
 // training step asks for the same again and again.
-nm_status choose_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw, GradArgs* a, int* grid, int* bn) {
+nm_status choose_grad(int64_t F, int64_t k, int64_t T, bool want_dx, bool want_dw, int pairs, GradArgs* a, int* grid,
+                      int* bn) {
   struct Key {
-    int64_t n_out, k, T;
+    int64_t F, k, T;
     int want, pairs, forced, whole;
     bool operator==(const Key& o) const {
-      return n_out == o.n_out && k == o.k && T == o.T && want == o.want && pairs == o.pairs && forced == o.forced &&
+      return F == o.F && k == o.k && T == o.T && want == o.want && pairs == o.pairs && forced == o.forced &&
              whole == o.whole;
     }
   };
@@ -862,9 +862,9 @@ nm_status choose_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw,
     int grid = 0, bn = 0;
   };
   static thread_local Choice last;
-  const int pairs = num_sms(h->device) / 2, forced = forced_grad_bn();
+  const int forced = forced_grad_bn();
   const char* split = getenv("NMSPMM_GRAD_SPLIT");  // 0: no split (tests and sweeps)
-  const Key key{h->n_out, h->k, T, (want_dx ? 1 : 0) + (want_dw ? 2 : 0), pairs, forced, split && split[0] == '0'};
+  const Key key{F, k, T, (want_dx ? 1 : 0) + (want_dw ? 2 : 0), pairs, forced, split && split[0] == '0'};
   if (last.bn && last.key == key) {
     *a = last.a;
     *grid = last.grid;
@@ -877,7 +877,7 @@ nm_status choose_grad(const nm_handle* h, int64_t T, bool want_dx, bool want_dw,
     if (forced && w != forced) continue;
     GradArgs c{};
     int g = 0;
-    const int64_t level = plan_grad(h, T, want_dx, want_dw, w, pairs, !key.whole, &c, &g);
+    const int64_t level = plan_grad(F, k, T, want_dx, want_dw, w, pairs, !key.whole, &c, &g);
     if (level < 0) return fail(NM_ERR_UNSUPPORTED, "T x k too large");
     const double cost = (double)level * (w == 256 ? 1.45 : 1.0);
     if (cost < best) {
@@ -929,6 +929,45 @@ nm_status nm_gated_backward_workspace(const nm_handle* h, int64_t T, size_t* byt
   if (st != NM_OK) return st;
   if (!bytes) return fail(NM_ERR_INVALID, "null output");
   *bytes = (size_t)GradWs(h, T).total;
+  return NM_OK;
+}
+
+nm_status nm_gated_backward_plan_for_shape(int64_t n_ff, int64_t k, int64_t T, int want_dx, int want_dw, int sms,
+                                           nm_grad_plan_info* out) {
+  clear_error();
+  if (!out) return fail(NM_ERR_INVALID, "null output");
+  if (n_ff <= 0 || k <= 0 || T <= 0 || sms < 2) return fail(NM_ERR_INVALID, "bad shape or SM count");
+  if (!want_dx && !want_dw) return fail(NM_ERR_INVALID, "nothing to compute");
+  if (n_ff > (1 << 23) || k > (1 << 24) || T > (int64_t(1) << 26)) return fail(NM_ERR_UNSUPPORTED, "shape too large");
+  GradArgs a{};
+  int grid = 0, bn = 0;
+  nm_status st = choose_grad(n_ff, k, T, want_dx != 0, want_dw != 0, sms / 2, &a, &grid, &bn);
+  if (st != NM_OK) return st;
+  *out = nm_grad_plan_info{};
+  out->bn = bn;
+  out->grid = grid;
+  for (const GradSide& g : a.side) {
+    if (!g.tiles) continue;
+    (g.dw ? out->splits_dw : out->splits_dx) = g.splits;
+    (g.dw ? out->runs_dw : out->runs_dx) = (g.per_split + kRunKb - 1) / kRunKb;
+  }
+  // every stage of every tile is some pair's, once; a cut tile's parts have slots of their own
+  int64_t stages = 0, want = (int64_t)a.side[0].tiles * a.side[0].n_kb + (int64_t)a.side[1].tiles * a.side[1].n_kb;
+  int64_t slots = 0, slot_sum = 0;
+  for (int pair = 0; pair < grid; ++pair) {
+    int64_t mine = 0;
+    GradUnit u;
+    for (int i = 0; grad_unit(a, pair, grid, i, bn, u); ++i) {
+      mine += u.kb1 - u.kb0;
+      if (u.slot >= 0) {
+        ++slots;
+        slot_sum += u.slot;
+      }
+    }
+    stages += mine;
+    out->stages = std::max<int64_t>(out->stages, mine);
+  }
+  out->complete = stages == want && slot_sum == slots * (slots - 1) / 2 && slots <= sms / 2;
   return NM_OK;
 }
 
@@ -985,7 +1024,8 @@ nm_status nm_gated_backward(const nm_handle* h, const void* X, const void* P, co
     return fail(NM_ERR_UNSUPPORTED, "T x n_ff too large");
   GradArgs a{};
   int bn = 0, grid = 0;
-  if ((dX || dW) && (st = choose_grad(h, T, dX != nullptr, dW != nullptr, &a, &grid, &bn)) != NM_OK) return st;
+  if ((dX || dW) && (st = choose_grad(F, h->k, T, dX != nullptr, dW != nullptr, sms / 2, &a, &grid, &bn)) != NM_OK)
+    return st;
   if ((a.side[0].splits > 1 || a.side[1].splits > 1) && lay.partial == lay.runs)
     return fail(NM_ERR_INVALID, "the workspace has no room for partial tiles");
   cudaError_t e = cudaSuccess;

@@ -18,7 +18,7 @@ import pytest
 import torch
 
 import structured_sparse_gemm_compress_b200 as nm
-from test_gpu_gated import dp_reference
+from test_gpu_gated import check_backward, dp_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -217,3 +217,23 @@ def test_range_is_decided_in_the_captured_call():
         graph.replay()
         for a, b in zip(out, want[i]):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ sums cut over idle pairs
+
+@pytest.mark.parametrize("bn", [128, 256])
+@pytest.mark.parametrize("dt", list(DTS))
+@pytest.mark.parametrize("T,k,F", [(1500, 64, 1500), (3000, 128, 700), (3000, 64, 1500), (1500, 72, 1501)])
+def test_both_products_cut(monkeypatch, T, k, F, dt, bn):
+    """Parts of both products' tiles in one call: slots and joined tiles of the second come after
+    the first's.  The same results every time, and from calls for one product alone."""
+    monkeypatch.setenv("NMSPMM_FORCE_GRAD_BN", str(bn))
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    plan = nm.nm_gated_backward_plan_for_shape(F, k, T, sms)
+    assert plan["splits_dx"] > 1 and plan["splits_dw"] > 1 and plan["complete"] == 1
+    h, X, P, dY, (dX, dW, db) = check_backward(dt, T, k, F, seed=T)
+    for _ in range(5):
+        x, w, b = nm.nm_gated_backward(h, X.cuda(), P.cuda(), dY.cuda(), bias_grad=True)
+        assert torch.equal(x, dX) and torch.equal(w, dW) and torch.equal(b, db)
+    if dt == "fp16":        # and the parts of a scaled dp
+        check_range(T, k, F, (2.0 ** -9, 300.0, 300.0, 2.0 ** -9), "silu", seed=T)
