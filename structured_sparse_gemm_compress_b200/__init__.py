@@ -235,7 +235,7 @@ def nm_recompress(h: NMHandle, W: torch.Tensor, stream=None) -> NMHandle:
 
 def out_dtype(h: NMHandle, scaled: bool) -> torch.dtype:
     if h.dt == NM_INT8:
-        return torch.float32 if scaled else torch.int32
+        return torch.float32 if scaled or h.gated else torch.int32
     return h.dtype
 
 
@@ -293,8 +293,9 @@ def resolve_out(h: NMHandle, out: str, scale, bias, act: str) -> str:
     if out != "default":
         return out
     if h.dtype == torch.int8:
-        return "int32" if scale is None and bias is None and act == "none" else "float32"
-    return "float16" if h.dtype == torch.float16 else "bfloat16"
+        raw = scale is None and bias is None and act == "none" and not getattr(h, "gated", False)
+        return "int32" if raw else "float32"
+    return {torch.float16: "float16", torch.bfloat16: "bfloat16", torch.float32: "float32"}[h.dtype]
 
 
 def nm_spmm_ex(h: NMHandle, X: torch.Tensor, Y: torch.Tensor | None = None, scale: torch.Tensor | None = None,
