@@ -131,8 +131,10 @@ __device__ __forceinline__ int dp_exponent(uint32_t peak) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// One pass over P and dY: dp [T][2][pitch] in the handle's type (rounded for the
-// tensor core; columns n_ff .. pitch are never read) and, with `part`, the fp32
+// One pass over P and dY: dp [T][2][pitch] in the handle's type (columns n_ff .. pitch
+// are never read; the rounding is that of the products' tensor-core operand, as in
+// mixed-precision training: it adds as much error, by rms, as the rounding of dX and dW
+// themselves, and two terms of dp would double the products) and, with `part`, the fp32
 // column sums of this block's rows ([row block][2][n_ff]), each warp's rows in
 // ascending order, the warps in order.  Memory bound: 48-51 us for 6304 x 2 x 4096
 // bf16 with the weight unpacked beside it (246 MB of DRAM traffic, 5 TB/s).

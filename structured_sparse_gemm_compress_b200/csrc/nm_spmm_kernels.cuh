@@ -502,10 +502,13 @@ __device__ __forceinline__ void gate_run(const SpmmArgs& a, const EpiCh& e, cons
 //   6304 x 1024 -> 2 x 4096    65.4 / 51.2   (70.3 / 53.9)
 //   12608 x 768 -> 2 x 2048    56.7 / 43.8   (62.9 / 46.1)
 //   6304 x 512 -> 2 x 2048     25.3 / 22.3   (32.0 / 22.5)
-// What bounds it: L2.  At the first size 0.92 / 0.75 GB cross it (operands of every
-// tile, and the output), 14 to 15 TB/s with and without p; MMAs are active 39 / 48 %
-// of the time, instruction issue 40 / 42 %, and a fifth stage in place of a second
-// staging buffer gains nothing (52.9 without p).
+// What bounds it, from copies with parts left out, first size, 64.0 / 50.0 in that run:
+// the operand copies alone take 34.6 (0.73 GB at 21 TB/s), with the MMAs 40.3, and with
+// the arithmetic and staging of the output 44.2; its stores, which share L2 and the SMs'
+// way to it with the copies, add 5.8 without p (52 MB) and 20 with it (155 MB).  INT8
+// (14 TB/s of half as many operand bytes: 20.5, 21.7, 30.2 with fp16 output, 34.7 with
+// its stores) is bound by the output stage; INT8 output is staged byte by byte, which
+// takes 7.4 more (44.4).  A fifth stage in place of a second staging buffer gains nothing.
 constexpr int kGateTok = 16;            // tokens of one step
 constexpr int kGateY = kGateTok * 128;  // staged Y bytes (64 channels of 16 bits; INT8 uses half)
 constexpr int kGateP = kGateTok * 256;  // staged p bytes: [token][gate, up][64 channels]
