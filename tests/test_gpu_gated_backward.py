@@ -219,6 +219,21 @@ def test_range_is_decided_in_the_captured_call():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("split", ["0", "1"])
+@pytest.mark.parametrize("down", [2.0 ** -14, 2.0 ** -10])
+def test_long_sums_of_a_scaled_dp(monkeypatch, down, split):
+    """Runs, parts and the scaling together: dp below fp16's normal range, exact once it is scaled."""
+    monkeypatch.setenv("NMSPMM_GRAD_SPLIT", split)
+    for T, k, F in ((1 << 18, 64, 16), (48, 64, 1 << 17)):
+        h, X, P, dY, W, dp = one_sign(torch.float16, T, k, F, seed=1)
+        dX, dW, db = backward(h, X, P, dY * (2 * down), "none")
+        dp = dp.double() * (2 * down)
+        close(dX, dp, W, 2 * F)
+        close(dW, dp.t(), X, T)
+        ref = dp.sum(0)
+        assert bool(((db.double() - ref).abs() <= (T / 8 + 24) * 2.0 ** -24 * ref).all())
+
+
 # ------------------------------------------------------------------ sums cut over idle pairs
 
 @pytest.mark.parametrize("bn", [128, 256])
